@@ -98,7 +98,8 @@ typedef enum {
   TP_OP_EMBED_BWD = 5,    /* pass (T, h, v, N): T tokens */
   TP_OP_LINEAR_XENT = 6,  /* pass (T, h, v, N) */
   TP_OP_SP_LN_BWD = 7,    /* pass (M, h, h, N): M token rows of width h */
-  TP_OP_ATTENTION_BWD = 8 /* pass (b·s, n_heads, 64, N) */
+  TP_OP_ATTENTION_BWD = 8, /* pass (b·s, n_heads, 64, N) */
+  TP_OP_LINEAR_LOGPROBS = 9 /* pass (T, h, v, N) */
 } tp_op;
 
 /*
@@ -563,6 +564,125 @@ TP_API tp_status tp_linear_xent_dlogits(const void* H, const void* E, const int6
                                         const float* lse, int64_t T, int64_t h, int64_t v,
                                         int32_t N, float grad_scale, void* dlogits,
                                         int32_t* dev_status, void* stream);
+
+/*
+ * Log-probabilities of given tokens, entropy and top alternatives
+ *   [TP-ILL] §5 (the vocabulary parts combine by their maxima and rescaled
+ *   sums; here the same rule also carries the entropy's sum and the parts'
+ *   best entries).  For scoring, policy-gradient training and decoding; the
+ *   pages print no formula beyond the softmax itself.
+ *
+ *   With z = scale·logits (scale: the inverse temperature) and, per row t,
+ *     lse[t]     = log Σ_j exp(z_j)                       fp32 [T]  (nullable)
+ *     logprob[t] = z_y − lse,  y = targets[t]             fp32 [T]  (nullable)
+ *     entropy[t] = −Σ_j p_j·log p_j,  p = exp(z − lse)    fp32 [T]  (nullable)
+ *     top_idx, top_logprob [T, top_k] (int32, fp32): the top_k largest
+ *       logits in descending order, equal values in index order (+0 equals
+ *       −0), and their log-probabilities.
+ *
+ *   logits [T,v], bf16 or fp32 (dt), 16-byte aligned; any v (rows need no
+ *   alignment); v % N == 0 (the shards are memory partitions; no output
+ *   depends on N).  targets [T] int64, NULL when logprob is NULL.
+ *   0 <= top_k <= min(v, 128) (TP_ERR_UNSUPPORTED above 128).  scale finite
+ *   and > 0 (else TP_ERR_SHAPE).  At least one output.
+ *   A target outside [0, v) sets TP_DEVERR_RANGE and gives logprob NaN; the
+ *   row's other outputs stay right.  Logits of −inf (banned tokens) have
+ *   probability 0 and add nothing to the entropy; a given token among them
+ *   has logprob −inf.  A row of nothing but −inf has no distribution: lse
+ *   −inf, every other number NaN.  A NaN or +inf logit makes the numbers of
+ *   its row NaN (lse too, or +inf); NaN entries are never among the
+ *   alternatives, and slots that no entry fills hold index −1 and NaN.
+ */
+TP_API tp_status vp_logprobs_fwd(const void* logits, tp_dtype dt, const int64_t* targets,
+                                 int64_t T, int64_t v, int32_t N, float scale, int32_t top_k,
+                                 float* logprob, float* entropy, float* lse, int32_t* top_idx,
+                                 float* top_logprob, int32_t* dev_status, void* stream);
+
+/*
+ * Its gradient with respect to the logits.
+ *
+ *   dlogits_j = scale·( g·[j = y] − p_j·(g + e·(z_j − lse + entropy)) )
+ *
+ *   with g = dlogprob[t] and e = dentropy[t] (fp32 [T]; either NULL: zero).
+ *   lse and entropy from vp_logprobs_fwd at the same scale (entropy NULL
+ *   without dentropy, targets NULL without dlogprob).  The alternatives
+ *   carry no gradient.  dlogits [T,v] bf16 or fp32 (grad_dt), 16-byte
+ *   aligned; it may be the logits themselves when grad_dt == dt, and must
+ *   not overlap them otherwise.
+ *   A row with g == 0 and e == 0 (padding) gets a row of zeros and is not
+ *   read, whatever its target, lse or logits.  A row with g != 0 whose
+ *   target lies outside [0, v) is NaN and sets TP_DEVERR_RANGE.
+ */
+TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t* targets,
+                                 const float* lse, const float* entropy, const float* dlogprob,
+                                 const float* dentropy, int64_t T, int64_t v, int32_t N,
+                                 float scale, void* dlogits, tp_dtype grad_dt,
+                                 int32_t* dev_status, void* stream);
+
+/*
+ * Distillation from a teacher's top entries: loss and gradient in one call
+ *   [TP-ILL] §5 with the one-hot target replaced by the teacher's
+ *   probabilities on K listed tokens.
+ *
+ *   Row t lists K slots (teacher_ids [T,K] int32, teacher_logits [T,K]
+ *   fp32); id −1 marks an empty slot.  Over the filled slots
+ *     renormalize != 0:  p_k = softmax_k(teacher_logits)
+ *     renormalize == 0:  p_k = exp(teacher_logits), i.e. log-probabilities
+ *                        (the mass of the unlisted tokens is left out)
+ *   and with q = softmax(scale·logits), P = Σ_k p_k, w = weight[t] (NULL: 1)
+ *     loss[t]  = w·Σ_k p_k·(log p_k − log q_{id_k})                fp32 [T]
+ *     loss_sum = Σ_t loss[t] in a fixed order              fp32 [1], nullable
+ *     lse[t]   = log Σ_j exp(scale·logits_j)               fp32 [T], nullable
+ *     dlogits  = grad_scale·∂loss_sum/∂logits
+ *              = grad_scale·w·scale·(P·q_j − Σ_{k: id_k = j} p_k)  [T,v], nullable
+ *   (teacher_logits are taken as given: divide them by the teacher's
+ *   temperature beforehand.)  A token listed twice counts twice.
+ *
+ *   logits [T,v] bf16 or fp32 (dt), dlogits grad_dt, both 16-byte aligned,
+ *   any v; dlogits may be the logits themselves when grad_dt == dt and must
+ *   not overlap them otherwise.  1 <= K <= 256 (TP_ERR_UNSUPPORTED above).
+ *   scale finite and > 0.  v % N == 0; no output depends on N.
+ *   A row with w == 0, or without a filled slot of probability above 0, has
+ *   loss 0 and a gradient of zeros, whatever its logits.  An id outside
+ *   [−1, v) in any other row sets TP_DEVERR_RANGE and makes that row's loss
+ *   and gradient NaN.  A listed token of probability above 0 whose logit is
+ *   −inf gives loss +inf.
+ */
+TP_API tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids,
+                            const float* teacher_logits, const float* weight, int64_t T,
+                            int64_t v, int32_t K, int32_t N, int32_t renormalize, float scale,
+                            float grad_scale, float* loss, float* loss_sum, float* lse,
+                            void* dlogits, tp_dtype grad_dt, int32_t* dev_status, void* stream);
+
+/*
+ * Output layer and log-probabilities in one pass, without the logits matrix
+ *   [TP-ILL] §4.2 and §5, as tp_linear_xent_fwd.
+ *
+ *   logprob, entropy and lse of vp_logprobs_fwd for logits = H·Eᵀ, from the
+ *   GEMM's fp32 accumulators: every 128-column slice of every row leaves its
+ *   maximum, Σ e and Σ e·(l − max), and a second kernel combines them.
+ *   H [T,h] bf16, E [v,h] bf16, h % 8 == 0, any v with v % N == 0; targets
+ *   [T] int64, NULL when logprob is NULL; each output nullable, at least one
+ *   given.  Out-of-range targets as in vp_logprobs_fwd.
+ *   ws, ws_bytes >= tp_workspace_bytes(TP_OP_LINEAR_LOGPROBS, T, h, v, N).
+ */
+TP_API tp_status tp_linear_logprobs_fwd(const void* H, const void* E, const int64_t* targets,
+                                        int64_t T, int64_t h, int64_t v, int32_t N, float scale,
+                                        float* logprob, float* entropy, float* lse, void* ws,
+                                        size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Its gradient at the logits, recomputed: vp_logprobs_bwd's dlogits for
+ * logits = H·Eᵀ, bf16 [T,v], the input of tp_logits_bwd.  The logits are
+ * rebuilt by the GEMM in fp32 and never stored.  v % 8 == 0, h % 8 == 0, H, E
+ * and dlogits 16-byte aligned.  Rows without upstream gradient are zero.
+ */
+TP_API tp_status tp_linear_logprobs_dlogits(const void* H, const void* E, const int64_t* targets,
+                                            const float* lse, const float* entropy,
+                                            const float* dlogprob, const float* dentropy,
+                                            int64_t T, int64_t h, int64_t v, int32_t N,
+                                            float scale, void* dlogits, int32_t* dev_status,
+                                            void* stream);
 
 #ifdef __cplusplus
 }

@@ -33,13 +33,15 @@ __all__ = [
     "tp_linear_xent_fwd", "tp_linear_xent_dlogits", "OP_LINEAR_XENT", "tp_mlp_bwd_recompute",
     "tp_attention_fwd", "tp_sp_dropout_add_ln_fwd", "tp_sp_dropout_add_ln_bwd", "OP_SP_LN_BWD",
     "tp_attention_bwd", "OP_ATTENTION_BWD",
+    "vp_logprobs_fwd", "vp_logprobs_bwd", "vp_distill",
+    "tp_linear_logprobs_fwd", "tp_linear_logprobs_dlogits", "OP_LINEAR_LOGPROBS",
     "OP_MLP_FWD", "OP_MLP_BWD", "OP_ROW_LINEAR_FWD", "OP_COL_LINEAR_BWD", "OP_ROW_LINEAR_BWD",
 ]
 
 ACT_NONE, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2
 DTYPE_BF16, DTYPE_F32 = 0, 1
 (OP_MLP_FWD, OP_MLP_BWD, OP_ROW_LINEAR_FWD, OP_COL_LINEAR_BWD, OP_ROW_LINEAR_BWD, OP_EMBED_BWD,
- OP_LINEAR_XENT, OP_SP_LN_BWD, OP_ATTENTION_BWD) = range(9)
+ OP_LINEAR_XENT, OP_SP_LN_BWD, OP_ATTENTION_BWD, OP_LINEAR_LOGPROBS) = range(10)
 DEVERR_RANGE, DEVERR_TIMEOUT = 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -87,6 +89,16 @@ _SIGS = {
     "tp_attention_bwd": ([_P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _I32, _F, _P, _P, _SZ,
                           _P, _P], _I32),
     "tp_attention_fwd": ([_P, _I64, _I64, _I32, _I32, _I32, _P, _I32, _F, _P, _P, _P, _P], _I32),
+    "vp_logprobs_fwd": ([_P, _I32, _P, _I64, _I64, _I32, _F, _I32, _P, _P, _P, _P, _P, _P, _P],
+                        _I32),
+    "vp_logprobs_bwd": ([_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I32, _F, _P, _I32, _P, _P],
+                        _I32),
+    "vp_distill": ([_P, _I32, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _F, _F, _P, _P, _P, _P,
+                    _I32, _P, _P], _I32),
+    "tp_linear_logprobs_fwd": ([_P, _P, _P, _I64, _I64, _I64, _I32, _F, _P, _P, _P, _P, _SZ, _P,
+                                _P], _I32),
+    "tp_linear_logprobs_dlogits": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _F, _P,
+                                    _P, _P], _I32),
     "tp_mlp_bwd_recompute": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _I32, _I32,
                               _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I32),
 }
@@ -673,3 +685,151 @@ def tp_attention_bwd(QKV, ctx, dctx, lse, b, s, n_heads, N, *, head_offsets=None
                                   _ptr(dQKV), _ptr(ws), wsb, _ptr(dev_status), _stream(dev)),
            "tp_attention_bwd")
     return dQKV
+
+
+def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, entropy=None,
+                    lse=None, top_idx=None, top_logprob=None, dev_status=None):
+    """Log-probability of targets[t] (None: left out), entropy, log-sum-exp and the top_k
+    alternatives of scale·logits, logits [T, v] bf16 or fp32.
+
+    Returns {"logprob" [T] or None, "entropy" [T], "lse" [T], "top_idx" [T, top_k] int32 or None,
+    "top_logprob" [T, top_k] or None}, fp32 unless named."""
+    T, v = logits.shape
+    dev = logits.device
+    if targets is None and logprob is not None:
+        raise ValueError("logprob needs targets")
+    if logprob is None and targets is not None:
+        logprob = torch.empty(T, dtype=torch.float32, device=dev)
+    entropy = torch.empty(T, dtype=torch.float32, device=dev) if entropy is None else entropy
+    lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
+    if top_k > 0:
+        if top_idx is None:
+            top_idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
+        if top_logprob is None:
+            top_logprob = torch.empty(T, top_k, dtype=torch.float32, device=dev)
+    elif top_idx is not None or top_logprob is not None:
+        raise ValueError("top_idx and top_logprob need top_k > 0")
+    _contig(logits, targets, logprob, entropy, lse, top_idx, top_logprob)
+    _want(dev, ("targets", targets, (T,), _I64T), ("logprob", logprob, (T,), _F32),
+          ("entropy", entropy, (T,), _F32), ("lse", lse, (T,), _F32),
+          ("top_idx", top_idx, (T, top_k), _I32T), ("top_logprob", top_logprob, (T, top_k), _F32),
+          _status_spec(dev_status))
+    _check(_launch(lib().vp_logprobs_fwd, dev, _ptr(logits), _dt(logits), _ptr(targets), T, v,
+                   N, float(scale), int(top_k), _ptr(logprob), _ptr(entropy), _ptr(lse),
+                   _ptr(top_idx), _ptr(top_logprob), _ptr(dev_status)), "vp_logprobs_fwd")
+    return {"logprob": logprob, "entropy": entropy, "lse": lse, "top_idx": top_idx,
+            "top_logprob": top_logprob}
+
+
+def _launch(fn, dev, *args):
+    """fn(*args, stream) on dev's current stream, with dev current during the call (the library
+    launches on the current device)."""
+    stream = _stream(dev)
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
+
+
+def _logprob_grad_args(targets, entropy, dlogprob, dentropy):
+    if dlogprob is None and dentropy is None:
+        raise ValueError("give dlogprob, dentropy or both")
+    if dlogprob is not None and targets is None:
+        raise ValueError("dlogprob needs targets")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+
+
+def vp_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, N, *, scale=1.0,
+                    grad_dtype=torch.bfloat16, dlogits=None, dev_status=None):
+    """Gradient of vp_logprobs_fwd's logprob and entropy at the logits: [T, v] in grad_dtype, or
+    in the type of ``dlogits`` when that is given (the logits themselves for in place).
+    dlogprob or dentropy may be None.  Returns dlogits."""
+    T, v = logits.shape
+    dev = logits.device
+    _logprob_grad_args(targets, entropy, dlogprob, dentropy)
+    if dlogits is None:
+        dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
+    _contig(logits, targets, lse, entropy, dlogprob, dentropy, dlogits)
+    _want(dev, ("targets", targets, (T,), _I64T), ("lse", lse, (T,), _F32),
+          ("entropy", entropy, (T,), _F32), ("dlogprob", dlogprob, (T,), _F32),
+          ("dentropy", dentropy, (T,), _F32), ("dlogits", dlogits, (T, v), None),
+          _status_spec(dev_status))
+    _check(_launch(lib().vp_logprobs_bwd, dev, _ptr(logits), _dt(logits), _ptr(targets),
+                   _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy), T, v, N,
+                   float(scale), _ptr(dlogits), _dt(dlogits), _ptr(dev_status)),
+                   "vp_logprobs_bwd")
+    return dlogits
+
+
+def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weight=None,
+               scale=1.0, grad_scale=1.0, with_grad=True, grad_dtype=torch.bfloat16, loss=None,
+               loss_sum=None, lse=None, dlogits=None, dev_status=None):
+    """Loss of softmax(scale·logits) against a teacher's listed entries (ids [T, K] int32, −1 for
+    an empty slot; logits [T, K] fp32, or log-probabilities with renormalize=False), and its
+    gradient at the logits in grad_dtype (or the type of ``dlogits``).
+
+    Returns {"loss" [T], "loss_sum" [1], "lse" [T], "dlogits" [T, v] or None}."""
+    T, v = logits.shape
+    dev = logits.device
+    K = teacher_ids.shape[1]
+    loss = torch.empty(T, dtype=torch.float32, device=dev) if loss is None else loss
+    loss_sum = torch.empty(1, dtype=torch.float32, device=dev) if loss_sum is None else loss_sum
+    lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
+    if with_grad and dlogits is None:
+        dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
+    _contig(logits, teacher_ids, teacher_logits, weight, loss, loss_sum, lse, dlogits)
+    _want(dev, ("teacher_ids", teacher_ids, (T, K), _I32T),
+          ("teacher_logits", teacher_logits, (T, K), _F32), ("weight", weight, (T,), _F32),
+          ("loss", loss, (T,), _F32), ("loss_sum", loss_sum, (1,), _F32), ("lse", lse, (T,), _F32),
+          ("dlogits", dlogits, (T, v), None), _status_spec(dev_status))
+    _check(_launch(lib().vp_distill, dev, _ptr(logits), _dt(logits), _ptr(teacher_ids),
+                   _ptr(teacher_logits), _ptr(weight), T, v, K, N, 1 if renormalize else 0,
+                   float(scale), float(grad_scale), _ptr(loss), _ptr(loss_sum), _ptr(lse),
+                   _ptr(dlogits), DTYPE_BF16 if dlogits is None else _dt(dlogits),
+                   _ptr(dev_status)), "vp_distill")
+    return {"loss": loss, "loss_sum": loss_sum, "lse": lse, "dlogits": dlogits}
+
+
+def tp_linear_logprobs_fwd(H, E, targets, N, *, scale=1.0, logprob=None, entropy=None, lse=None,
+                           ws=None, dev_status=None):
+    """vp_logprobs_fwd's logprob (targets None: left out), entropy and lse of logits = H·Eᵀ
+    without storing the logits.  Returns {"logprob", "entropy", "lse"}, fp32 [T]."""
+    T, h = H.shape
+    v = E.shape[0]
+    dev = H.device
+    if targets is None and logprob is not None:
+        raise ValueError("logprob needs targets")
+    if logprob is None and targets is not None:
+        logprob = torch.empty(T, dtype=torch.float32, device=dev)
+    entropy = torch.empty(T, dtype=torch.float32, device=dev) if entropy is None else entropy
+    lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
+    _contig(H, E, targets, logprob, entropy, lse)
+    _want(dev, ("H", H, (T, h), _BF), ("E", E, (v, h), _BF), ("targets", targets, (T,), _I64T),
+          ("logprob", logprob, (T,), _F32), ("entropy", entropy, (T,), _F32),
+          ("lse", lse, (T,), _F32), _ws_spec(ws), _status_spec(dev_status))
+    ws, wsb = _workspace(ws, OP_LINEAR_LOGPROBS, T, h, v, N, dev)
+    _check(_launch(lib().tp_linear_logprobs_fwd, dev, _ptr(H), _ptr(E), _ptr(targets), T, h, v,
+                   N, float(scale), _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(ws), wsb,
+                   _ptr(dev_status)), "tp_linear_logprobs_fwd")
+    return {"logprob": logprob, "entropy": entropy, "lse": lse}
+
+
+def tp_linear_logprobs_dlogits(H, E, targets, lse, entropy, dlogprob, dentropy, N, *, scale=1.0,
+                               dlogits=None, dev_status=None):
+    """bf16 gradient of tp_linear_logprobs_fwd's outputs at the logits [T, v] (the input of
+    tp_logits_bwd), the logits recomputed on chip.  dlogprob or dentropy may be None."""
+    T, h = H.shape
+    v = E.shape[0]
+    dev = H.device
+    _logprob_grad_args(targets, entropy, dlogprob, dentropy)
+    dlogits = torch.empty(T, v, dtype=torch.bfloat16, device=dev) if dlogits is None else dlogits
+    _contig(H, E, targets, lse, entropy, dlogprob, dentropy, dlogits)
+    _want(dev, ("H", H, (T, h), _BF), ("E", E, (v, h), _BF), ("targets", targets, (T,), _I64T),
+          ("lse", lse, (T,), _F32), ("entropy", entropy, (T,), _F32),
+          ("dlogprob", dlogprob, (T,), _F32), ("dentropy", dentropy, (T,), _F32),
+          ("dlogits", dlogits, (T, v), _BF), _status_spec(dev_status))
+    _check(_launch(lib().tp_linear_logprobs_dlogits, dev, _ptr(H), _ptr(E), _ptr(targets),
+                   _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy), T, h, v, N,
+                   float(scale), _ptr(dlogits), _ptr(dev_status)), "tp_linear_logprobs_dlogits")
+    return dlogits

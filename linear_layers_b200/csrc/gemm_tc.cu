@@ -64,6 +64,13 @@ constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 64 + kEpiThreads;
 
+// Epilogues over the rows' softmax (the loss and log-probability statistics
+// and gradients): 256-column tiles, no split.
+constexpr bool softmax_epi(int epi) {
+  return epi == EPI_XENT_STATS || epi == EPI_XENT_GRAD || epi == EPI_LOGP_STATS ||
+         epi == EPI_LOGP_GRAD;
+}
+
 struct GemmArgs {
   int M, N, K;
   int a_mn, b_mn;
@@ -93,6 +100,11 @@ struct GemmArgs {
   float* tgt_logit;
   const float* row_lse;
   float grad_scale;
+  float* stat_u;                    // EPI_LOGP_*
+  const float* row_entropy;
+  const float* row_dlp;
+  const float* row_de;
+  float logit_scale;
   int inject_unit, inject_kb;       // debug: the producer stops before this k-block (-1: never)
   int tma_out;                      // bf16 outputs leave through tensor maps (tmO)
 };
@@ -399,8 +411,8 @@ template <int CG, int BNT, int RH, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_constant__ GemmParams P) {
   using C = Cfg<CG, BNT, RH>;
   static_assert(RH == 1 || (CG == 2 && BNT == 256), "tall tiles are 2-CTA 256-column tiles");
-  static_assert(BNT == 256 || (EPI != EPI_XENT_STATS && EPI != EPI_XENT_GRAD),
-                "the cross-entropy epilogues take 128-column slices of a 256-column tile");
+  static_assert(BNT == 256 || !softmax_epi(EPI),
+                "the softmax epilogues take 128-column slices of a 256-column tile");
   constexpr int STAGES = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -838,6 +850,112 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           if (row_ok)
             store_bf16x32(static_cast<__nv_bfloat16*>(a.out0) + row * a.ldo + col0, v, a.N - col0);
         }
+      } else if constexpr (EPI == EPI_LOGP_STATS) {
+        // Log-probability statistics of this warp's 128-column slice of each
+        // row, on z = scale·acc: the maximum m of acc, s = Σ e and
+        // u = Σ e·(acc − m) with e = exp(scale·(acc − m)).  When m grows by δ
+        // both sums are rescaled by α = exp(−scale·δ): s ← α·s,
+        // u ← α·(u − δ·s).  The thread whose slice holds the row's target
+        // keeps that accumulator.
+        const int slice = tn * (BNT / kXentSlice) + half;
+        if (slice * kXentSlice < a.N) {   // warp-uniform
+          const int64_t tgt = row_ok && a.targets ? a.targets[row] : -1;
+          const float sl = a.logit_scale * kLog2e;
+          float m = -INFINITY, ssum = 0.0f, usum = 0.0f;
+#pragma unroll 1
+          for (int c = c0; c < c0 + C::kChunks; ++c) {
+            const int col0 = tn * BNT + c * 32;
+            if (col0 >= a.N) break;        // warp-uniform
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_base + c * 32, r);
+            tc_wait_ld();
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            if (col0 + 32 > a.N) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col0 + j >= a.N) v[j] = -INFINITY;
+            }
+            if (tgt >= col0 && tgt < col0 + 32) {
+              float tl = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col0 + j == tgt) tl = v[j];
+              a.tgt_logit[row] = tl;
+            }
+            float cm[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              cm[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
+            const float cmax = fmaxf(fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])),
+                                     fmaxf(fmaxf(cm[4], cm[5]), fmaxf(cm[6], cm[7])));
+            const float mn = fmaxf(m, cmax);
+            const float mr = mn == -INFINITY ? 0.0f : mn;   // a row of −inf so far adds zeros
+            float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f}, pu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float d = v[j] - mr;
+              const float e = ex2_approx(d * sl);
+              ps[j & 3] += e;
+              // −inf columns: e = 0 against a finite factor
+              pu[j & 3] = fmaf(e, fmaxf(d, -1e30f), pu[j & 3]);
+            }
+            const float dm = m == -INFINITY ? 0.0f : m - mr;
+            const float al = ex2_approx(dm * sl);
+            usum = fmaf(al, fmaf(dm, ssum, usum), (pu[0] + pu[1]) + (pu[2] + pu[3]));
+            ssum = fmaf(ssum, al, (ps[0] + ps[1]) + (ps[2] + ps[3]));
+            m = mn;
+          }
+          if (row_ok) {
+            const int64_t o = static_cast<int64_t>(slice) * a.M + row;
+            a.stat_m[o] = m;
+            a.stat_s[o] = ssum;
+            a.stat_u[o] = usum;
+          }
+        }
+      } else if constexpr (EPI == EPI_LOGP_GRAD) {
+        // With lp = scale·acc − lse, p = exp(lp), and the upstream gradients g
+        // (log-probability) and e (entropy) of the row:
+        //   out = scale·(g·[col = target] − p·(g + e·(lp + entropy)))
+        // A row without upstream gradient is zero whatever its logits; one
+        // whose target is needed and lies outside the vocabulary is NaN.
+        float lse = 0.0f, ent = 0.0f, g = 0.0f, e = 0.0f, bad = 0.0f;
+        int64_t tgt = -1;
+        if (row_ok) {
+          lse = a.row_lse[row];
+          if (a.row_dlp) g = a.row_dlp[row];
+          if (a.row_de) e = a.row_de[row];
+          if (e != 0.0f) ent = a.row_entropy[row];
+          if (g != 0.0f) {
+            tgt = a.targets[row];
+            if (tgt < 0 || tgt >= a.N) {
+              bad = __int_as_float(0x7fc00000);
+              if (tn == 0 && half == 0 && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
+            }
+          }
+        }
+        const bool zero = g == 0.0f && e == 0.0f;
+        const float ls = a.logit_scale;
+        const float geh = fmaf(e, ent, g);       // g + e·entropy
+#pragma unroll 1
+        for (int c = c0; c < c0 + C::kChunks; ++c) {
+          const int col0 = tn * BNT + c * 32;
+          if (col0 >= a.N) break;          // warp-uniform
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_base + c * 32, r);
+          tc_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float lp = fmaf(__uint_as_float(r[j]), ls, -lse);
+            const float p = ex2_approx(lp * kLog2e);
+            const float d = (col0 + j == tgt ? g : 0.0f) - p * fmaf(e, fmaxf(lp, -1e30f), geh);
+            v[j] = zero ? 0.0f : fmaf(ls, d, bad);
+          }
+          if (row_ok)
+            store_bf16x32(static_cast<__nv_bfloat16*>(a.out0) + row * a.ldo + col0, v, a.N - col0);
+        }
       } else {
         uint4 aux_w[4];
         constexpr bool kDact = EPI == EPI_DACT || EPI == EPI_DACT_Y;
@@ -1130,6 +1248,12 @@ tp_status launch_epi(const GemmParams& prm, int epi, int slots, cudaStream_t str
     case EPI_XENT_GRAD:
       if constexpr (BNT == 256) return launch_impl<CG, BNT, RH, EPI_XENT_GRAD>(prm, slots, stream);
       break;
+    case EPI_LOGP_STATS:
+      if constexpr (BNT == 256) return launch_impl<CG, BNT, RH, EPI_LOGP_STATS>(prm, slots, stream);
+      break;
+    case EPI_LOGP_GRAD:
+      if constexpr (BNT == 256) return launch_impl<CG, BNT, RH, EPI_LOGP_GRAD>(prm, slots, stream);
+      break;
   }
   return TP_ERR_UNSUPPORTED;
 }
@@ -1174,7 +1298,7 @@ double tile_efficiency(const TileChoice& t) {
 // single-CTA tiles; the cross-entropy epilogues need 256-column tiles.
 // TP_GEMM_TILE=2x256|2x256t|2x128|1x256|1x128 forces a shape (tests, sweeps).
 TileChoice choose_tile(int M, int N, int K, int splits, int epi) {
-  const bool xent = epi == EPI_XENT_STATS || epi == EPI_XENT_GRAD;
+  const bool xent = softmax_epi(epi);
   // the tall tile's epilogue does not overlap its main loop: only for long
   // main loops (K per split >= 4096) with bf16 outputs (the fp32 logits and
   // the cross-entropy epilogues stay on the overlapped tile)
@@ -1339,9 +1463,14 @@ tp_status setup_problem(const GemmProblem& p, const TileChoice& tile, GemmArgs& 
   a.tgt_logit = p.tgt_logit;
   a.row_lse = p.row_lse;
   a.grad_scale = p.grad_scale;
+  a.stat_u = p.stat_u;
+  a.row_entropy = p.row_entropy;
+  a.row_dlp = p.row_dlp;
+  a.row_de = p.row_de;
+  a.logit_scale = p.logit_scale;
   a.inject_unit = -1;
   a.inject_kb = -1;
-  if ((p.epi == EPI_XENT_STATS || p.epi == EPI_XENT_GRAD) && p.splits != 1) return TP_ERR_UNSUPPORTED;
+  if (softmax_epi(p.epi) && p.splits != 1) return TP_ERR_UNSUPPORTED;
   if (split_epi) {
     const size_t need = gemm_split_ws_bytes(p.M, p.N, p.splits, p.zpart != nullptr);
     if (p.ws == nullptr || p.ws_bytes < need) return TP_ERR_WORKSPACE;
@@ -1439,7 +1568,7 @@ tp_status gemm_tc_launch_pair(const GemmProblem& p0, const GemmProblem& p1, cuda
     }
   // two independent problems of one epilogue, no split, no partials: one launch
   if (p0.splits != 1 || p1.splits != 1 || p0.zpart || p1.zpart || p0.epi != p1.epi ||
-      p0.epi == EPI_XENT_STATS || p0.epi == EPI_XENT_GRAD || p0.dbias_part || p1.dbias_part)
+      softmax_epi(p0.epi) || p0.dbias_part || p1.dbias_part)
     return TP_ERR_UNSUPPORTED;
   // the tile shape of the larger problem, and pairs of CTAs only when both
   // are more than one 128-row tile high

@@ -22,8 +22,12 @@ enum EpiKind : int {
                         // maximum, Σ exp(acc − maximum), first arg-max; the target
                         // column's accumulator; no output matrix
   EPI_XENT_GRAD = 6,    // out0 = bf16(grad_scale·(exp(acc − lse_row) − [col = target]))
-  EPI_DACT_Y = 7        // EPI_DACT, and out1 = act(aux): the activation rebuilt from the
+  EPI_DACT_Y = 7,       // EPI_DACT, and out1 = act(aux): the activation rebuilt from the
                         // saved pre-activation (recompute), from the same tanh as act'
+  EPI_LOGP_STATS = 8,   // statistics of each 128-column slice of every row: maximum m,
+                        // Σ e and Σ e·(acc − m) with e = exp(scale·(acc − m)); the
+                        // target column's accumulator; no output matrix
+  EPI_LOGP_GRAD = 9     // out0 = bf16 gradient of (log-probability, entropy) at the logits
 };
 
 constexpr int kXentSlice = 128;   // columns per softmax-statistics slice
@@ -63,6 +67,13 @@ struct GemmProblem {
   float* tgt_logit = nullptr;        // [M] accumulator at the target column
   const float* row_lse = nullptr;    // [M] log-sum-exp of each row (EPI_XENT_GRAD)
   float grad_scale = 1.0f;
+  // EPI_LOGP_STATS / EPI_LOGP_GRAD (with targets, stat_m, stat_s, tgt_logit, row_lse above;
+  // targets nullable)
+  float* stat_u = nullptr;           // [ceil(N/128), M] slice sums of e·(acc − max)
+  const float* row_entropy = nullptr;   // [M] (EPI_LOGP_GRAD, with row_de)
+  const float* row_dlp = nullptr;    // [M] upstream gradient at the log-probability, nullable
+  const float* row_de = nullptr;     // [M] upstream gradient at the entropy, nullable
+  float logit_scale = 1.0f;          // z = logit_scale·acc
 };
 
 // Workspace a split GEMM needs: fp32 partial tiles (unless zpart carries
@@ -121,6 +132,64 @@ tp_status sp_ln_bwd_launch(const void* dy, const void* dhs_in, const void* hs, c
                            const float* mean, const float* rstd, int64_t M, int64_t h, float p,
                            uint64_t seed, uint64_t offset, void* dx, void* dres, float* dgamma,
                            float* dbeta, float* dbias, void* ws, cudaStream_t stream);
+
+// loss_sum = Σ_t loss[t] in a fixed order (vocab.cu).
+tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStream_t stream);
+
+// Log-probabilities, entropy and top alternatives, and their gradient
+// (logprobs.cu): see vp_logprobs_fwd / vp_logprobs_bwd.
+constexpr int kLogprobsMaxK = 128;
+struct LogprobsArgs {
+  const void* logits;
+  const int64_t* targets;   // nullable
+  int64_t T, v;
+  float scale;
+  int top_k;
+  float* logprob;           // nullable, as are entropy and lse
+  float* entropy;
+  float* lse;
+  int32_t* top_idx;         // [T, top_k]
+  float* top_logprob;
+  int32_t* dev_status;
+};
+struct LogprobsBwdArgs {
+  const void* logits;
+  const int64_t* targets;
+  const float* lse;
+  const float* entropy;
+  const float* dlogprob;    // nullable
+  const float* dentropy;    // nullable
+  int64_t T, v;
+  float scale;
+  void* dlogits;
+  int32_t* dev_status;
+};
+tp_status logprobs_fwd_launch(const LogprobsArgs& a, tp_dtype dt, cudaStream_t stream);
+tp_status logprobs_bwd_launch(const LogprobsBwdArgs& a, tp_dtype dt, tp_dtype grad_dt,
+                              cudaStream_t stream);
+tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_s,
+                                         const float* stat_u, const float* tgt_logit,
+                                         const int64_t* targets, int64_t T, int64_t v, float scale,
+                                         float* logprob, float* entropy, float* lse,
+                                         int32_t* dev_status, cudaStream_t stream);
+
+// Distillation from a teacher's top entries: see vp_distill.
+constexpr int kDistillMaxK = 256;
+struct DistillArgs {
+  const void* logits;
+  const int32_t* ids;       // [T, K], -1: empty slot
+  const float* teacher;     // [T, K]
+  const float* weight;      // [T], nullable
+  int64_t T, v;
+  int K, renormalize;
+  float scale, grad_scale;
+  float* loss;              // [T]
+  float* lse;               // [T], nullable
+  void* dlogits;            // nullable
+  int32_t* dev_status;
+};
+tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, float* loss_sum,
+                         cudaStream_t stream);
 
 // Counts every kernel the library enqueues (tp_launch_count).
 void note_launches(int n);

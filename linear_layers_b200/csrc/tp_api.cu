@@ -182,6 +182,21 @@ size_t linear_xent_ws_bytes(int64_t T, int64_t v) {
   return 3 * plane + align256(static_cast<size_t>(T) * 4);
 }
 
+// slice maxima, slice sums, slice sums of e·(x − max) ([ceil(v/128), T] each), target logits [T]:
+// the same planes as linear_xent_ws_bytes, with the third of floats
+size_t linear_logprobs_ws_bytes(int64_t T, int64_t v) { return linear_xent_ws_bytes(T, v); }
+
+// A softmax scale (inverse temperature): finite and positive.
+bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
+
+bool dtype_ok(tp_dtype dt) { return dt == TP_DTYPE_BF16 || dt == TP_DTYPE_F32; }
+
+bool words_aligned(std::initializer_list<const void*> ps, uintptr_t bytes) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) return false;
+  return true;
+}
+
 size_t dbias_ws(int64_t M, int64_t F) { return align256(((M + 31) / 32) * F * sizeof(float)); }
 
 // Run a row-parallel GEMM C[M,Nout] = Σ_i A[:, off_i:off_{i+1}]·B[off_i:off_{i+1}, :]
@@ -279,6 +294,8 @@ size_t tp_workspace_bytes(tp_op op, int64_t M, int64_t h, int64_t F, int32_t N) 
       return align256(embed_bwd_ws_bytes(M));
     case TP_OP_LINEAR_XENT:   // (T, h, v, N): slice statistics + target logits
       return linear_xent_ws_bytes(M, F);
+    case TP_OP_LINEAR_LOGPROBS:   // (T, h, v, N): slice statistics + target logits
+      return linear_logprobs_ws_bytes(M, F);
     case TP_OP_SP_LN_BWD:     // (M, h, h, N): per-block partial parameter gradients
       return sp_ln_bwd_ws_bytes(M, h);
     case TP_OP_ATTENTION_BWD: // (b·s, n_heads, 64, N): rowsum(dO ⊙ O), fp32 dQ accumulator
@@ -788,6 +805,126 @@ tp_status tp_linear_xent_dlogits(const void* H, const void* E, const int64_t* ta
   g.targets = targets;
   g.row_lse = lse;
   g.grad_scale = grad_scale;
+  g.dev_status = dev_status;
+  return gemm_tc_launch(g, as_stream(stream));
+}
+
+tp_status vp_logprobs_fwd(const void* logits, tp_dtype dt, const int64_t* targets, int64_t T,
+                          int64_t v, int32_t N, float scale, int32_t top_k, float* logprob,
+                          float* entropy, float* lse, int32_t* top_idx, float* top_logprob,
+                          int32_t* dev_status, void* stream) {
+  if (!logits || (!logprob && !entropy && !lse && top_k == 0) || (!targets && logprob))
+    return TP_ERR_NULL;
+  if (top_k > 0 && (!top_idx || !top_logprob)) return TP_ERR_NULL;
+  if (!dtype_ok(dt)) return TP_ERR_DTYPE;
+  if (!dims_ok({T, v}) || N < 1 || v % N || top_k < 0 || top_k > v || !scale_ok(scale))
+    return TP_ERR_SHAPE;
+  if (top_k > kLogprobsMaxK) return TP_ERR_UNSUPPORTED;
+  if (!aligned16(logits) || !words_aligned({targets}, 8) ||
+      !words_aligned({logprob, entropy, lse, top_idx, top_logprob}, 4))
+    return TP_ERR_ALIGN;
+  if (tp_status s = require_sm100()) return s;
+  LogprobsArgs a{logits, targets, T,   v,       scale,       top_k,
+                 logprob, entropy, lse, top_idx, top_logprob, dev_status};
+  return logprobs_fwd_launch(a, dt, as_stream(stream));
+}
+
+tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t* targets,
+                          const float* lse, const float* entropy, const float* dlogprob,
+                          const float* dentropy, int64_t T, int64_t v, int32_t N, float scale,
+                          void* dlogits, tp_dtype grad_dt, int32_t* dev_status, void* stream) {
+  if (!logits || !lse || !dlogits || (!dlogprob && !dentropy) || (dlogprob && !targets) ||
+      (dentropy && !entropy))
+    return TP_ERR_NULL;
+  if (!dtype_ok(dt) || !dtype_ok(grad_dt)) return TP_ERR_DTYPE;
+  if (!dims_ok({T, v}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
+  if (!ptrs_aligned({logits, dlogits}) || !words_aligned({targets}, 8) ||
+      !words_aligned({lse, entropy, dlogprob, dentropy}, 4))
+    return TP_ERR_ALIGN;
+  if (logits == dlogits && dt != grad_dt) return TP_ERR_UNSUPPORTED;
+  if (tp_status s = require_sm100()) return s;
+  LogprobsBwdArgs a{logits, targets, lse, entropy, dlogprob, dentropy,
+                    T,      v,       scale, dlogits, dev_status};
+  return logprobs_bwd_launch(a, dt, grad_dt, as_stream(stream));
+}
+
+tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids,
+                     const float* teacher_logits, const float* weight, int64_t T, int64_t v,
+                     int32_t K, int32_t N, int32_t renormalize, float scale, float grad_scale,
+                     float* loss, float* loss_sum, float* lse, void* dlogits, tp_dtype grad_dt,
+                     int32_t* dev_status, void* stream) {
+  if (!logits || !teacher_ids || !teacher_logits || !loss) return TP_ERR_NULL;
+  if (!dtype_ok(dt) || (dlogits && !dtype_ok(grad_dt))) return TP_ERR_DTYPE;
+  if (!dims_ok({T, v, K}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
+  if (K > kDistillMaxK) return TP_ERR_UNSUPPORTED;
+  if (!ptrs_aligned({logits, dlogits}) ||
+      !words_aligned({teacher_ids, teacher_logits, weight, loss, loss_sum, lse}, 4))
+    return TP_ERR_ALIGN;
+  if (logits == dlogits && dt != grad_dt) return TP_ERR_UNSUPPORTED;
+  if (tp_status s = require_sm100()) return s;
+  DistillArgs a{logits, teacher_ids, teacher_logits, weight, T,   v,       K, renormalize != 0,
+                scale,  grad_scale,  loss,           lse,    dlogits, dev_status};
+  return distill_launch(a, dt, grad_dt, loss_sum, as_stream(stream));
+}
+
+tp_status tp_linear_logprobs_fwd(const void* H, const void* E, const int64_t* targets, int64_t T,
+                                 int64_t h, int64_t v, int32_t N, float scale, float* logprob,
+                                 float* entropy, float* lse, void* ws, size_t ws_bytes,
+                                 int32_t* dev_status, void* stream) {
+  if (!H || !E || (!logprob && !entropy && !lse) || (!targets && logprob)) return TP_ERR_NULL;
+  if (!dims_ok({T, h, v}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
+  if (h % 8 || !ptrs_aligned({H, E}) || !words_aligned({targets}, 8) ||
+      !words_aligned({logprob, entropy, lse}, 4))
+    return TP_ERR_ALIGN;
+  const size_t need = linear_logprobs_ws_bytes(T, v);
+  if (ws == nullptr || ws_bytes < need) return TP_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return TP_ERR_ALIGN;
+  if (tp_status s = require_sm100()) return s;
+  const size_t plane = align256(static_cast<size_t>((v + kXentSlice - 1) / kXentSlice) * T * 4);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  GemmProblem g;
+  g.A = H; g.lda = h; g.a_mn = 0;
+  g.B = E; g.ldb = h; g.b_mn = 0;               // E [v,h] read as Eᵀ: K-major
+  g.M = static_cast<int>(T); g.N = static_cast<int>(v); g.K = static_cast<int>(h);
+  g.epi = EPI_LOGP_STATS;
+  g.targets = targets;
+  g.logit_scale = scale;
+  g.stat_m = reinterpret_cast<float*>(w);
+  g.stat_s = reinterpret_cast<float*>(w + plane);
+  g.stat_u = reinterpret_cast<float*>(w + 2 * plane);
+  g.tgt_logit = reinterpret_cast<float*>(w + 3 * plane);
+  g.dev_status = dev_status;
+  cudaStream_t st = as_stream(stream);
+  if (tp_status s = gemm_tc_launch(g, st)) return s;
+  return linear_logprobs_combine_launch(g.stat_m, g.stat_s, g.stat_u, g.tgt_logit, targets, T, v,
+                                        scale, logprob, entropy, lse, dev_status, st);
+}
+
+tp_status tp_linear_logprobs_dlogits(const void* H, const void* E, const int64_t* targets,
+                                     const float* lse, const float* entropy,
+                                     const float* dlogprob, const float* dentropy, int64_t T,
+                                     int64_t h, int64_t v, int32_t N, float scale, void* dlogits,
+                                     int32_t* dev_status, void* stream) {
+  if (!H || !E || !lse || !dlogits || (!dlogprob && !dentropy) || (dlogprob && !targets) ||
+      (dentropy && !entropy))
+    return TP_ERR_NULL;
+  if (!dims_ok({T, h, v}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
+  if (h % 8 || v % 8 || !ptrs_aligned({H, E, dlogits}) || !words_aligned({targets}, 8) ||
+      !words_aligned({lse, entropy, dlogprob, dentropy}, 4))
+    return TP_ERR_ALIGN;
+  if (tp_status s = require_sm100()) return s;
+  GemmProblem g;
+  g.A = H; g.lda = h; g.a_mn = 0;
+  g.B = E; g.ldb = h; g.b_mn = 0;
+  g.M = static_cast<int>(T); g.N = static_cast<int>(v); g.K = static_cast<int>(h);
+  g.epi = EPI_LOGP_GRAD;
+  g.out0 = dlogits; g.ldo = v;
+  g.targets = targets;
+  g.row_lse = lse;
+  g.row_entropy = entropy;
+  g.row_dlp = dlogprob;
+  g.row_de = dentropy;
+  g.logit_scale = scale;
   g.dev_status = dev_status;
   return gemm_tc_launch(g, as_stream(stream));
 }

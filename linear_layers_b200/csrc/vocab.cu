@@ -524,11 +524,15 @@ __global__ void __launch_bounds__(kCombWarps * 32) linear_xent_combine_kernel(
   }
 }
 
+}  // namespace
+
 tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStream_t stream) {
   loss_sum_kernel<<<1, 1024, 0, stream>>>(loss, T, loss_sum);
   note_launches(1);
   return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
+
+namespace {
 
 template <int R, int NT, typename GT>
 tp_status xent_cluster_launch(const float* logits, const int64_t* targets, int64_t T, int64_t v,

@@ -762,3 +762,113 @@ def embed_bwd_sharded(ids, dout, v, N):
 def tied_embedding_grad(dE_output, dE_input):
     """The shared table's gradient: output-layer part plus input-layer part."""
     return f64(dE_output) + f64(dE_input)
+
+
+# ----------------------------------------------------------------------------
+# Token log-probabilities, entropy, top alternatives; distillation ([TP-ILL] §5)
+# ----------------------------------------------------------------------------
+def logprobs(logits_, targets=None, scale=1.0, top_k=0):
+    """Per row, with z = scale·logits: lse = log Σ exp z, logprob = z_y − lse,
+    entropy = −Σ p·log p (p = exp(z − lse), 0·log 0 = 0) and the top_k entries
+    in descending order, equal values in index order.
+
+    Targets outside [0, v) give logprob NaN.  A row of nothing but −inf has no
+    distribution: lse −inf, every other number NaN.
+    """
+    L = f64(logits_)
+    T, v = L.shape
+    z = scale * L
+    with np.errstate(invalid="ignore", divide="ignore"):
+        m = z.max(axis=1)
+        log_s = np.log(np.exp(z - m[:, None]).sum(axis=1))
+        lse = np.where(m == -np.inf, -np.inf, m + log_s)
+        lp = (z - m[:, None]) - log_s[:, None]
+        p = np.exp(lp)
+        ent = -np.where(p > 0, p * lp, np.where(np.isnan(p), np.nan, 0.0)).sum(axis=1)
+    out = {"lse": lse, "entropy": ent, "logprob": None, "top_idx": None, "top_logprob": None}
+    if targets is not None:
+        y = i64(targets)
+        ok = (y >= 0) & (y < v)
+        out["logprob"] = np.full(T, np.nan)
+        out["logprob"][ok] = lp[np.nonzero(ok)[0], y[ok]]
+    if top_k:
+        idx = np.argsort(-L, axis=1, kind="stable")[:, :top_k]   # NaN entries sort last
+        rows = np.arange(T)[:, None]
+        filled = ~np.isnan(L[rows, idx])
+        out["top_idx"] = np.where(filled, idx, -1)
+        out["top_logprob"] = np.where(filled, lp[rows, idx], np.nan)
+    return out
+
+
+def logprobs_bwd(logits_, targets, dlogprob, dentropy, scale=1.0):
+    """Gradient of Σ_t dlogprob·logprob + dentropy·entropy at the logits.
+
+    ∂logprob/∂z_j = [j = y] − p_j,  ∂entropy/∂z_j = −p_j·(log p_j + entropy).
+    Rows whose two upstream gradients are zero are zero; rows with a target
+    outside [0, v) and dlogprob ≠ 0 are NaN.
+    """
+    L = f64(logits_)
+    T, v = L.shape
+    g = np.zeros(T) if dlogprob is None else f64(dlogprob)
+    e = np.zeros(T) if dentropy is None else f64(dentropy)
+    r = logprobs(L, None, scale)
+    with np.errstate(invalid="ignore"):
+        lp = scale * L - r["lse"][:, None]
+        p = np.exp(lp)
+        w = np.where(p > 0, lp + r["entropy"][:, None], 0.0)
+        d = -p * (g[:, None] + e[:, None] * w)
+    if dlogprob is not None:
+        y = i64(targets)
+        ok = (y >= 0) & (y < v)
+        d[np.nonzero(ok)[0], y[ok]] += g[ok]
+        d[~ok & (g != 0)] = np.nan
+    d *= scale
+    d[(g == 0) & (e == 0)] = 0.0
+    return d
+
+
+def distill(logits_, ids, teacher, renormalize=True, weight=None, scale=1.0, grad_scale=1.0):
+    """Loss of q = softmax(scale·logits) against a teacher's listed entries.
+
+    ids [T, K] (−1: empty slot), teacher [T, K]: p = softmax over the filled
+    slots, or exp(teacher) without renormalize.
+    loss_t = w_t·Σ_k p_k·(log p_k − log q_{id_k}),
+    dlogits = grad_scale·w_t·scale·(Σp·q − Σ_k p_k·onehot(id_k)).
+    Rows of weight 0 or without a slot of probability above 0 are zero; any
+    other row with an id outside [−1, v) is NaN.
+    """
+    L = f64(logits_)
+    T, v = L.shape
+    ids = i64(ids)
+    t = f64(teacher).copy()
+    w = np.ones(T) if weight is None else f64(weight)
+    filled = (ids >= 0) & (ids < v)
+    bad = ((ids < -1) | (ids >= v)).any(axis=1)
+    t[~filled] = -np.inf
+    lse = logprobs(L, None, scale)["lse"]
+    loss = np.zeros(T)
+    d = np.zeros((T, v))
+    P = np.zeros(T)
+    for r in range(T):
+        with np.errstate(invalid="ignore", divide="ignore"):
+            if renormalize:
+                top = t[r].max()
+                lp = t[r] - (np.log(np.exp(t[r] - top).sum()) + top if top > -np.inf else 0.0)
+            else:
+                lp = t[r]
+            p = np.exp(lp)
+            p[~filled[r]] = 0.0
+            live = p > 0
+            P[r] = p.sum()
+            if w[r] == 0 or (not live.any() and not bad[r]):
+                continue
+            if bad[r]:
+                loss[r] = np.nan
+                d[r] = np.nan
+                continue
+            lq = scale * L[r] - lse[r]
+            loss[r] = w[r] * np.sum(p[live] * (lp[live] - lq[ids[r][live]]))
+            d[r] = P[r] * np.exp(lq)
+            np.subtract.at(d[r], ids[r][live], p[live])
+            d[r] *= grad_scale * w[r] * scale
+    return {"loss": loss, "loss_sum": loss.sum(), "lse": lse, "dlogits": d, "P": P}

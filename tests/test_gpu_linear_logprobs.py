@@ -1,0 +1,145 @@
+"""Log-probabilities and entropy without the logits matrix, and their gradient,
+on the GPU against the fp64 oracle.
+
+The GEMM adds h products in fp32, at most h/16 roundings of partial sums of
+size ~10 or less: below 1e-3 of a logit for h <= 4096, and the log-probability
+and entropy follow the logits one to one, so the bar is TOL_XENT relative to
+values of 8 or more, as for the cross-entropy without the logits.  The bf16
+gradient has the bf16 bar.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import linear_layers_b200 as tpl
+import tp_inputs
+from oracle import tp_oracle as O
+from tests.gpu_helpers import TOL_BF16, TOL_XENT, assert_close, f64, guarded
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(T, v, h, seed):
+    inp = tp_inputs.vocab_inputs(T, v, h, e_std=1.6 / math.sqrt(h), seed=seed)
+    return inp["H"], inp["E"], inp["targets"]
+
+
+def _check_fwd(r, ref):
+    for k in ("logprob", "entropy", "lse"):
+        got, want = f64(r[k]), ref[k]
+        assert np.array_equal(np.isnan(got), np.isnan(want)), k
+        ok = ~np.isnan(want)
+        assert np.all(np.abs(got[ok] - want[ok]) <= TOL_XENT * np.maximum(np.abs(want[ok]), 4.0)), k
+
+
+SHAPES = [(1, 2048, 64, 8), (300, 1000, 256, 4), (16, 2048, 64, 8), (200, 136, 512, 2),
+          (513, 4096, 328, 1), (3, 50304, 1600, 4), (130, 8, 8, 1)]
+
+
+@pytest.mark.parametrize("T,v,h,N", SHAPES)
+@pytest.mark.parametrize("scale", [1.0, 0.6])
+def test_forward_and_gradient(T, v, h, N, scale):
+    H, E, y = _inputs(T, v, h, seed=T)
+    st = tpl.new_status()
+    Hd, Ed, yd = H.cuda(), E.cuda(), y.cuda()
+    bufs, guards = {}, []
+    for k in ("logprob", "entropy", "lse"):
+        bufs[k], g = guarded((T,), torch.float32)
+        guards.append(g)
+    r = tpl.tp_linear_logprobs_fwd(Hd, Ed, yd, N, scale=scale, dev_status=st, **bufs)
+    for g in guards:
+        g.check()
+    L = O.logits(H, E)
+    _check_fwd(r, O.logprobs(L, y, scale))
+    gen = torch.Generator().manual_seed(1)
+    dlp, de = torch.randn(T, generator=gen), 0.2 * torch.randn(T, generator=gen)
+    if T > 2:
+        dlp[1], de[1] = 0.0, 0.0
+    out, guard = guarded((T, v), torch.bfloat16)
+    for a, b in ((dlp, de), (dlp, None), (None, de)):
+        tpl.tp_linear_logprobs_dlogits(Hd, Ed, yd, r["lse"], r["entropy"],
+                                       None if a is None else a.cuda(),
+                                       None if b is None else b.cuda(), N, scale=scale, dlogits=out,
+                                       dev_status=st)
+        guard.check("dlogits")
+        want = O.logprobs_bwd(L, y, a, b, scale)
+        assert_close("dlogits", out, want, TOL_BF16)
+        if T > 2:
+            assert not out[1].any()
+    assert int(st.item()) == 0
+
+
+def test_forward_of_an_odd_vocabulary_without_targets():
+    H, E, _ = _inputs(70, 1003, 64, seed=5)
+    r = tpl.tp_linear_logprobs_fwd(H.cuda(), E.cuda(), None, 1)
+    ref = O.logprobs(O.logits(H, E))
+    assert r["logprob"] is None
+    for k in ("entropy", "lse"):
+        assert np.all(np.abs(f64(r[k]) - ref[k]) <= TOL_XENT * np.maximum(np.abs(ref[k]), 4.0))
+
+
+def test_bad_targets_and_padded_rows():
+    T, v = 40, 520
+    H, E, y = _inputs(T, v, 64, seed=6)
+    y = y.clone()
+    y[3], y[7] = -1, v
+    st = tpl.new_status()
+    r = tpl.tp_linear_logprobs_fwd(H.cuda(), E.cuda(), y.cuda(), 2, dev_status=st)
+    L = O.logits(H, E)
+    _check_fwd(r, O.logprobs(L, y))
+    assert int(st.item()) == tpl.DEVERR_RANGE
+    g = torch.ones(T)
+    g[7] = 0.0                                   # padded: zero, not flagged
+    st = tpl.new_status()
+    d = tpl.tp_linear_logprobs_dlogits(H.cuda(), E.cuda(), y.cuda(), r["lse"], None, g.cuda(), None,
+                                       2, dev_status=st)
+    assert int(st.item()) == tpl.DEVERR_RANGE
+    assert torch.isnan(d[3]).all() and not d[7].any()
+    g[3] = 0.0
+    st = tpl.new_status()
+    d = tpl.tp_linear_logprobs_dlogits(H.cuda(), E.cuda(), y.cuda(), r["lse"], None, g.cuda(), None,
+                                       2, dev_status=st)
+    assert int(st.item()) == 0
+    assert_close("dlogits", d, O.logprobs_bwd(L, y, g, None), TOL_BF16)
+
+
+def test_policy_step_matches_the_path_through_the_logits():
+    """Hidden states to log-probabilities, the gradient at the logits and the
+    output layer's backward: without the logits matrix, and through it."""
+    T, v, h = 160, 4096, 256
+    H, E, y = (a.cuda() for a in _inputs(T, v, h, seed=7))
+    adv = torch.randn(T, generator=torch.Generator().manual_seed(3)).cuda() / T
+    de = torch.full((T,), -0.01 / T, device="cuda")
+    a = tpl.tp_linear_logprobs_fwd(H, E, y, 4, scale=1.25)
+    da = tpl.tp_linear_logprobs_dlogits(H, E, y, a["lse"], a["entropy"], adv, de, 4, scale=1.25)
+    L = tpl.tp_logits_fwd(H, E, 4)
+    b = tpl.vp_logprobs_fwd(L, y, 4, scale=1.25)
+    db = tpl.vp_logprobs_bwd(L, y, b["lse"], b["entropy"], adv, de, 4, scale=1.25)
+    for k in ("logprob", "entropy", "lse"):
+        # the same accumulators, summed in another order: 2·B of 4096 columns and roundings
+        assert float((a[k] - b[k]).abs().max()) < 1e-4, k
+    ga, gb = tpl.tp_logits_bwd(da, H, E, 4), tpl.tp_logits_bwd(db, H, E, 4)
+    for p, q in zip(ga, gb):
+        assert_close("gradient", p, f64(q), TOL_BF16)
+
+
+def test_workspace_is_shared_by_two_captured_graphs_in_turn():
+    T, v, h = 64, 1000, 128
+    H, E, y = (a.cuda() for a in _inputs(T, v, h, seed=8))
+    ws = torch.empty(tpl.tp_workspace_bytes(tpl.OP_LINEAR_LOGPROBS, T, h, v, 1), dtype=torch.uint8,
+                     device="cuda")
+    want = tpl.tp_linear_logprobs_fwd(H, E, y, 1)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = tpl.tp_linear_logprobs_fwd(H, E, y, 1, ws=ws)
+        graphs.append((g, r))
+    for g, _ in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for _, r in graphs:
+        for k in want:
+            assert torch.equal(r[k], want[k]), k
