@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
               // −inf columns: e = 0 against a finite factor
               pu[j & 3] = fmaf(e, fmaxf(d, -1e30f), pu[j & 3]);
             }
-            const float dm = m == -INFINITY ? 0.0f : m - mr;
+            const float dm = m == -INFINITY ? 0.0f : fmaxf(m - mr, -1e30f);
             const float al = ex2_approx(dm * sl);
             usum = fmaf(al, fmaf(dm, ssum, usum), (pu[0] + pu[1]) + (pu[2] + pu[3]));
             ssum = fmaf(ssum, al, (ps[0] + ps[1]) + (ps[2] + ps[3]));

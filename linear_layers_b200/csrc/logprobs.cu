@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "internal.h"
@@ -20,8 +21,10 @@
 namespace tpl {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -1e30f;   // stands for what lies below it in products with a zero probability
 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -29,11 +32,179 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// max(a, b), NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Logits are read once: 16-byte units that do not stay in L1.
+__device__ __forceinline__ uint4 ld_unit(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <typename IT>
+struct Unit;   // the elements of 16 bytes
+template <>
+struct Unit<float> {
+  static constexpr int kN = 4;
+  static constexpr uint32_t kMinusInf = 0xff800000u;
+  static __device__ __forceinline__ void unpack(uint4 w, float* x) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+};
+template <>
+struct Unit<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static constexpr uint32_t kMinusInf = 0xff80ff80u;
+  static __device__ __forceinline__ void unpack(uint4 w, float* x) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(q[i] << 16);
+      x[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    }
+  }
+};
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// N consecutive gradient elements at p (N·sizeof aligned to 8 bytes or more)
+template <int N>
+__device__ __forceinline__ void put_unit(float* p, const float* x) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    __stcs(reinterpret_cast<float4*>(p) + i,
+           make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+}
+template <int N>
+__device__ __forceinline__ void put_unit(__nv_bfloat16* p, const float* x) {
+  if constexpr (N == 4)
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])));
+  else
+    __stcs(reinterpret_cast<uint4*>(p),
+           make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7])));
+}
+
+// A row of v elements from flat element f0 of a 16-byte-aligned matrix: `head`
+// elements up to the first 16-byte boundary, `units` whole units, `tail`.
+// Rows of any length are read in aligned units this way, and nothing outside
+// the row is touched.
+template <typename IT>
+struct RowShape {
+  int head, units, tail;
+  __device__ __forceinline__ RowShape(int64_t f0, int64_t v) {
+    constexpr int n = Unit<IT>::kN;
+    head = static_cast<int>((-f0) & (n - 1));
+    if (head > v) head = static_cast<int>(v);
+    units = static_cast<int>((v - head) / n);
+    tail = static_cast<int>(v - head) - units * n;
+  }
+};
+
+// Running softmax sums of one thread over raw logits: s = Σ e, u = Σ e·(x − r)
+// with e = exp(scale·(x − r)).  The reference r moves only when a logit
+// exceeds it by more than 8 in log2 units, so e stays below 2^8 and the
+// rescaling is rare; any reference gives the same result.  A thread that has
+// seen no logit above −inf keeps r = 0 with the threshold at −inf.
+struct RowSums {
+  float ref = 0.0f, above = -INFINITY;
+  float2 s = {0.0f, 0.0f}, u = {0.0f, 0.0f};
+
+  template <int N, bool kEntropy>
+  __device__ __forceinline__ float add(const float (&x)[N], float sl, float tau) {
+    float mx = max3f(fmaxf(x[0], x[1]), x[2], x[3]);
+#pragma unroll
+    for (int i = 4; i < N; i += 4) mx = max3f(max3f(mx, x[i], x[i + 1]), x[i + 2], x[i + 3]);
+    if (mx > above) {
+      const float dm = above == -CUDART_INF_F ? 0.0f : max_nan(ref - mx, kLowest);
+      const float al = ex2_approx(dm * sl);
+      if (kEntropy)
+        u = make_float2(al * fmaf(dm, s.x, u.x), al * fmaf(dm, s.y, u.y));
+      s = make_float2(al * s.x, al * s.y);
+      ref = mx;
+      above = mx + tau;
+    }
+    const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float2 d = __fadd2_rn(make_float2(x[i], x[i + 1]), nr);
+      if (kEntropy) d = make_float2(max_nan(d.x, kLowest), max_nan(d.y, kLowest));
+      const float2 y = __fmul2_rn(d, sl2);
+      const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+      s = __fadd2_rn(s, e);
+      if (kEntropy) u = __ffma2_rn(e, d, u);
+    }
+    return mx;
+  }
+  // one element (the row's edges)
+  template <bool kEntropy>
+  __device__ __forceinline__ void add1(float x, float sl, float tau) {
+    const float q[4] = {x, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+    add<4, kEntropy>(q, sl, tau);
+  }
+};
+
+// The sums of several threads, on a common reference: m = −inf where nothing
+// above −inf was seen.
+struct Sums {
+  float m, s, u;
+};
+
+__device__ __forceinline__ Sums warp_sums(const RowSums& r, float sl) {
+  Sums a{r.above == -CUDART_INF_F ? -CUDART_INF_F : r.ref, r.s.x + r.s.y, r.u.x + r.u.y};
+  float m = a.m;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float d = max_nan(a.m - (m == -CUDART_INF_F ? 0.0f : m), kLowest);
+  const float f = ex2_approx(d * sl);
+  float s = a.s * f, u = f * fmaf(d, a.s, a.u);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, off);
+    u += __shfl_xor_sync(0xffffffffu, u, off);
+  }
+  return Sums{m, s, u};
+}
+
+// n sums in order, the same in every caller
+template <typename F>
+__device__ __forceinline__ Sums join_sums(int n, float sl, F get) {
+  float m = -CUDART_INF_F;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, get(i).m);
+  const float r = m == -CUDART_INF_F ? 0.0f : m;
+  float s = 0.0f, u = 0.0f;
+  for (int i = 0; i < n; ++i) {
+    const Sums q = get(i);
+    const float d = max_nan(q.m - r, kLowest);
+    const float f = ex2_approx(d * sl);
+    s = fmaf(q.s, f, s);
+    u = fmaf(f, fmaf(d, q.s, q.u), u);
+  }
+  return Sums{m, s, u};
+}
+
+// ---------------------------------------------------------------------------
+// top alternatives
+// ---------------------------------------------------------------------------
 // Descending value, then ascending index, as one unsigned order: 0 is "no
 // entry" (NaN never enters).  +0 and −0 are the same value.
 __device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
@@ -49,182 +220,347 @@ __device__ __forceinline__ int32_t key_index(uint64_t key) {
   return static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key));
 }
 
-template <typename V, typename F>
-__device__ __forceinline__ V block_reduce(V x, V* sh, F f) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, off));
-  if (lane == 0) sh[warp] = x;
-  __syncthreads();
-  x = sh[0];
-  for (int w = 1; w < kRowThreads / 32; ++w) x = f(x, sh[w]);
-  __syncthreads();
-  return x;
+// The r-th largest of the warp's keys (distinct but for 0), 0 if there are fewer.
+__device__ __forceinline__ uint64_t warp_rth_key(uint64_t key, int r) {
+  uint64_t best = 0;
+  for (int i = 0; i < r; ++i) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+    const uint32_t lo = __reduce_max_sync(
+        0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
+    best = (static_cast<uint64_t>(hi) << 32) | lo;
+    if (key == best) key = 0;
+  }
+  return best;
 }
 
-// One block per row: maximum, sums, then the alternatives one by one.
-template <typename IT>
-__global__ void __launch_bounds__(kRowThreads) logprobs_row_kernel(const LogprobsArgs a) {
-  __shared__ float sf[kRowThreads / 32];
-  __shared__ uint64_t sk[kRowThreads / 32];
-  const int64_t t = blockIdx.x;
-  const IT* row = static_cast<const IT*>(a.logits) + t * a.v;
-  float m = -CUDART_INF_F;
-  for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) m = fmaxf(m, to_f32(row[j]));
-  m = block_reduce(m, sf, [](float p, float q) { return fmaxf(p, q); });
-  if (m == -CUDART_INF_F) m = 0.0f;   // nothing but −inf (or NaN): S is 0 (or NaN)
-  float s = 0.0f, u = 0.0f;
-  const float sl = a.scale * kLog2e;
-  for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) {
-    const float d = to_f32(row[j]) - m;
-    const float e = ex2_approx(d * sl);
-    s += e;
-    u = fmaf(e, fmaxf(d, -1e30f), u);
+// Candidates for the row's top k in shared memory, more than enough of them:
+// every element at or above a threshold that at least k elements reach.  The
+// threshold is the smallest over the warps of the ceil(k/8)-th largest of the
+// lanes' maxima.  When more than kLimit candidates have gathered, the
+// threshold is raised among them and the rest dropped; the buffer has room
+// for kLimit and one more step of the whole block, so it cannot overflow.
+template <int kStep>
+struct Candidates {
+  static constexpr int kLimit = 512;
+  static constexpr int kRoom = kLimit + kStep + 16;
+  uint64_t key[kRoom];
+  uint64_t warp_key[kWarps];
+  uint64_t kth;
+  int n, kept;
+
+  // Smallest over the warps of the r-th largest key held by their lanes.
+  __device__ __forceinline__ uint64_t threshold(uint64_t lane_key, int k) {
+    const uint64_t w = warp_rth_key(lane_key, (k + kWarps - 1) / kWarps);
+    if ((threadIdx.x & 31) == 0) warp_key[threadIdx.x >> 5] = w;
+    __syncthreads();
+    uint64_t t = warp_key[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) t = t < warp_key[i] ? t : warp_key[i];
+    return t;
   }
-  auto add = [](float p, float q) { return p + q; };
-  s = block_reduce(s, sf, add);
-  u = block_reduce(u, sf, add);
-  const float log_s = logf(s);
-  if (threadIdx.x == 0) {
-    if (a.targets) {
-      const int64_t y = a.targets[t];
-      const bool ok = y >= 0 && y < a.v;
-      if (!ok && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
-      if (a.logprob) a.logprob[t] = ok ? fmaf(a.scale, to_f32(row[y]) - m, -log_s) : CUDART_NAN_F;
+  // Keeps the candidates that `keep(i, key)` accepts; all threads, after a
+  // barrier.  Blocks of candidates move down in order: what a block writes
+  // lies below what the later blocks read.
+  template <typename F>
+  __device__ __forceinline__ int compact(int count, F keep) {
+    if (threadIdx.x == 0) kept = 0;
+    for (int base = 0; base < count; base += kThreads) {
+      const int i = base + static_cast<int>(threadIdx.x);
+      const uint64_t q = i < count ? key[i] : 0;
+      const bool ok = i < count && keep(i, q);
+      __syncthreads();
+      if (ok) key[atomicAdd(&kept, 1)] = q;
     }
-    if (a.entropy) a.entropy[t] = log_s - a.scale * (u / s);
-    if (a.lse) a.lse[t] = fmaf(a.scale, m, log_s);
+    __syncthreads();
+    const int left = kept;
+    __syncthreads();
+    return left;
   }
-  uint64_t last = ~0ull;
-  for (int k = 0; k < a.top_k; ++k) {
+  // Fewer candidates, the top k among them; raises t.  All threads, after a
+  // barrier; ends with one.
+  __device__ __forceinline__ int shrink(int count, int k, uint64_t& t) {
     uint64_t best = 0;
-    for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) {
-      const float x = to_f32(row[j]);
-      const uint64_t key = x == x ? rank_key(x, static_cast<uint32_t>(j)) : 0;
-      if (key < last && key > best) best = key;
-    }
-    best = block_reduce(best, sk, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
-    if (threadIdx.x == 0) {
-      const int64_t o = t * a.top_k + k;
-      a.top_idx[o] = best ? key_index(best) : -1;
-      a.top_logprob[o] = best ? fmaf(a.scale, key_value(best) - m, -log_s) : CUDART_NAN_F;
-    }
-    last = best;
+    for (int i = threadIdx.x; i < count; i += kThreads) best = best > key[i] ? best : key[i];
+    const uint64_t low = threshold(best, k);
+    if (low > t) t = low;
+    const uint64_t floor_key = t;
+    return compact(count, [=](int, uint64_t q) { return q >= floor_key; });
   }
+  // The same down to k exactly (count² / 256 comparisons a thread): for
+  // orders of values that the threshold does not thin out.
+  __device__ __forceinline__ int shrink_exact(int count, int k, uint64_t& t) {
+    uint32_t flags = 0;
+    static_assert((kRoom + kThreads - 1) / kThreads <= 32, "one flag per candidate of a thread");
+    for (int i = threadIdx.x, b = 0; i < count; i += kThreads, ++b) {
+      const uint64_t q = key[i];
+      int rank = 0;
+      for (int j = 0; j < count; ++j) rank += key[j] > q;
+      if (rank < k) flags |= 1u << b;
+      if (rank == k - 1) kth = q;
+    }
+    __syncthreads();
+    const int left = compact(count, [=](int i, uint64_t) { return (flags >> (i / kThreads)) & 1u; });
+    if (left == k && kth > t) t = kth;
+    return left;
+  }
+};
+
+// Log-probability statistics of one row by `slices` blocks (a cluster), each
+// taking a contiguous range of the row's 16-byte units.  A block streams its
+// range with the next step's loads in flight while it adds up the present
+// one; sums and candidates of the blocks meet in block 0 through distributed
+// shared memory.  Reading the row once is the bound: 256 threads hold 64 bytes
+// each in flight.
+template <typename IT, bool kTop>
+__global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
+    logprobs_kernel(const LogprobsArgs a, int slices) {
+  constexpr int kN = Unit<IT>::kN;
+  constexpr int kUnits = 2;                       // units per thread and step
+  constexpr int kStep = kThreads * kUnits * kN;   // elements per step
+  using Cand = Candidates<kTop ? kStep : 0>;
+  extern __shared__ __align__(16) uint8_t dyn_smem[];
+  Cand& cand = *reinterpret_cast<Cand*>(dyn_smem);   // only touched with kTop
+  __shared__ Sums wsum[kWarps];
+  __shared__ Sums bsum;
+  __shared__ uint64_t best[kTop ? kLogprobsMaxK : 1];
+
+  const int rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t t = blockIdx.x / static_cast<unsigned>(slices);
+  const int64_t f0 = t * a.v;
+  const RowShape<IT> shape(f0, a.v);
+  const IT* row = static_cast<const IT*>(a.logits) + f0;
+  const IT* body = row + shape.head;
+  const int per = (shape.units + slices - 1) / slices;
+  const int u0 = min(rank * per, shape.units), u1 = min(u0 + per, shape.units);
+  const int tid = threadIdx.x;
+  const float sl = a.scale * kLog2e;
+  const float tau = 8.0f / sl;
+
+  // the given token's logit, in flight behind the row
+  int64_t y = -1;
+  float xy = 0.0f;
+  const bool want_y = rank == 0 && tid == 0 && a.targets != nullptr;
+  if (want_y) {
+    y = a.targets[t];
+    if (y >= 0 && y < a.v) xy = to_f32(row[y]);
+  }
+
+  const uint4 fill = make_uint4(Unit<IT>::kMinusInf, Unit<IT>::kMinusInf, Unit<IT>::kMinusInf,
+                                Unit<IT>::kMinusInf);
+  auto load = [&](int base, uint4 (&w)[kUnits]) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = base + i * kThreads + tid;
+      w[i] = u < u1 ? ld_unit(body + static_cast<int64_t>(u) * kN) : fill;
+    }
+  };
+
+  RowSums sums;
+  [[maybe_unused]] uint64_t floor_key = 0;           // threshold of the candidates
+  [[maybe_unused]] float floor_x = CUDART_NAN_F;     // its value; NaN admits everything
+  [[maybe_unused]] bool full = false;                // a candidate landed at or past kLimit
+  auto admit = [&](uint64_t q) {
+    if constexpr (kTop) {
+      const int at = atomicAdd(&cand.n, 1);
+      cand.key[at] = q;
+      full |= at >= Cand::kLimit;
+    }
+  };
+
+  uint4 next[kUnits];
+  load(u0, next);
+  if constexpr (kTop) {
+    if (tid == 0) cand.n = 0;
+    __syncthreads();
+  }
+  const int steps = (u1 - u0 + kThreads * kUnits - 1) / (kThreads * kUnits);
+  for (int st = 0; st < steps; ++st) {
+    const int base = u0 + st * kThreads * kUnits;
+    float x[kUnits * kN];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) Unit<IT>::unpack(next[i], x + i * kN);
+    if (st + 1 < steps) load(base + kThreads * kUnits, next);
+    const float mx = sums.add<kUnits * kN, true>(x, sl, tau);
+    if constexpr (kTop) {
+      auto index = [&](int i) {   // within the row
+        return static_cast<uint32_t>(shape.head + (base + (i / kN) * kThreads + tid) * kN + i % kN);
+      };
+      auto inside = [&](int i) { return base + (i / kN) * kThreads + tid < u1; };
+      if (st == 0) {
+        // first threshold, from the lanes' maxima of this step
+        uint64_t lane_key = 0;
+#pragma unroll
+        for (int i = kUnits * kN - 1; i >= 0; --i)
+          if (x[i] == mx && inside(i)) lane_key = rank_key(mx, index(i));
+        floor_key = cand.threshold(lane_key, a.top_k);
+        floor_x = floor_key ? key_value(floor_key) : CUDART_NAN_F;
+#pragma unroll
+        for (int i = 0; i < kUnits * kN; ++i)
+          if (!(x[i] < floor_x) && x[i] == x[i] && inside(i)) {
+            const uint64_t q = rank_key(x[i], index(i));
+            if (q >= floor_key) admit(q);
+          }
+      } else if (!(mx <= floor_x)) {
+        // later elements equal to the threshold's value come behind it
+#pragma unroll
+        for (int i = 0; i < kUnits * kN; ++i)
+          if (!(x[i] <= floor_x) && x[i] == x[i] && inside(i)) admit(rank_key(x[i], index(i)));
+      }
+      if (__syncthreads_or(full)) {
+        int left = cand.shrink(cand.n, a.top_k, floor_key);
+        if (left > Cand::kLimit / 2) left = cand.shrink_exact(left, a.top_k, floor_key);
+        floor_x = floor_key ? key_value(floor_key) : CUDART_NAN_F;
+        full = false;
+        if (tid == 0) cand.n = left;
+        __syncthreads();
+      }
+    }
+  }
+  // the edges of the row: at most kN − 1 elements at each end
+  auto edge = [&](int j) {
+    const float x = to_f32(row[j]);
+    sums.add1<true>(x, sl, tau);
+    if constexpr (kTop) {
+      const uint64_t q = x == x ? rank_key(x, static_cast<uint32_t>(j)) : 0;
+      if (q >= floor_key && q) admit(q);
+    }
+  };
+  if (rank == 0 && tid < shape.head) edge(tid);
+  if (rank == slices - 1 && tid >= 32 && tid < 32 + shape.tail)
+    edge(shape.head + shape.units * kN + tid - 32);
+
+  const Sums w = warp_sums(sums, sl);
+  if ((tid & 31) == 0) wsum[tid >> 5] = w;
+  __syncthreads();
+  Sums all = join_sums(kWarps, sl, [&](int i) { return wsum[i]; });
+
+  // this block's best: a count of the candidates, rank by rank
+  [[maybe_unused]] auto ranked = [&](int n, auto&& out) {
+    if constexpr (kTop) {
+      if (n > 2 * a.top_k + 64) n = cand.shrink(n, a.top_k, floor_key);
+      for (int i = tid; i < n; i += kThreads) {
+        const uint64_t q = cand.key[i];
+        int rank_of = 0;
+        for (int j = 0; j < n; ++j) rank_of += cand.key[j] > q;
+        if (rank_of < a.top_k) out(rank_of, q);
+      }
+      for (int i = n + tid; i < a.top_k; i += kThreads) out(i, 0);   // slots nothing fills
+    }
+  };
+  if (slices > 1) {
+    if constexpr (kTop) ranked(cand.n, [&](int i, uint64_t q) { best[i] = q; });
+    if (tid == 0) bsum = all;
+    cluster_sync_all();
+    if (rank == 0) {
+      all = join_sums(slices, sl, [&](int i) {
+        const uint32_t at = mapa_shared(&bsum, static_cast<uint32_t>(i));
+        Sums q;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.m) : "r"(at));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(at + 4));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.u) : "r"(at + 8));
+        return q;
+      });
+      if constexpr (kTop) {
+        if (tid == 0) cand.n = 0;
+        __syncthreads();
+        for (int i = tid; i < slices * a.top_k; i += kThreads) {
+          uint64_t q;
+          asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                       : "=l"(q)
+                       : "r"(mapa_shared(&best[i % a.top_k], static_cast<uint32_t>(i / a.top_k))));
+          if (q) admit(q);
+        }
+        floor_key = 0;
+        __syncthreads();
+      }
+    }
+    cluster_sync_all();   // the peers' shared memory has been read
+    if (rank != 0) return;
+  }
+
+  const float ref = all.m == -CUDART_INF_F ? 0.0f : all.m;
+  const float log_s = logf(all.s);
+  if (want_y) {
+    const bool ok = y >= 0 && y < a.v;
+    if (!ok && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
+    if (a.logprob) a.logprob[t] = ok ? fmaf(a.scale, xy - ref, -log_s) : CUDART_NAN_F;
+  }
+  if (tid == 0) {
+    if (a.entropy) a.entropy[t] = log_s - a.scale * (all.u / all.s);
+    if (a.lse) a.lse[t] = fmaf(a.scale, ref, log_s);
+  }
+  if constexpr (kTop)
+    ranked(cand.n, [&](int i, uint64_t q) {
+      const int64_t o = t * a.top_k + i;
+      a.top_idx[o] = q ? key_index(q) : -1;
+      a.top_logprob[o] = q ? fmaf(a.scale, key_value(q) - ref, -log_s) : CUDART_NAN_F;
+    });
 }
+
+// Gradient of (log-probability, entropy): one pass over the logits, each
+// block a contiguous range of one row, every thread's loads of its (up to)
+// four units in flight at once.
+constexpr int kBwdUnits = 4;
 
 template <typename IT, typename GT>
-__global__ void __launch_bounds__(kRowThreads) logprobs_bwd_kernel(const LogprobsBwdArgs a) {
-  const int64_t t = blockIdx.x;
-  const IT* row = static_cast<const IT*>(a.logits) + t * a.v;
-  GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
+__global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobsBwdArgs a, int blocks) {
+  constexpr int kN = Unit<IT>::kN;
+  const int64_t t = blockIdx.x / static_cast<unsigned>(blocks);
+  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks));
+  const int64_t f0 = t * a.v;
+  const RowShape<IT> shape(f0, a.v);
+  const IT* row = static_cast<const IT*>(a.logits) + f0;
+  GT* out = static_cast<GT*>(a.dlogits) + f0;
+  const int per = (shape.units + blocks - 1) / blocks;
+  const int u0 = min(part * per, shape.units), u1 = min(u0 + per, shape.units);
+  const int tid = threadIdx.x;
   const float g = a.dlogprob ? a.dlogprob[t] : 0.0f;
   const float e = a.dentropy ? a.dentropy[t] : 0.0f;
-  if (g == 0.0f && e == 0.0f) {
-    for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) put(out + j, 0.0f);
-    return;
+  const bool zero = g == 0.0f && e == 0.0f;   // a padded row: nothing of it is read
+  uint4 w[kBwdUnits];
+#pragma unroll
+  for (int i = 0; i < kBwdUnits; ++i) {
+    const int u = u0 + i * kThreads + tid;
+    w[i] = !zero && u < u1 ? ld_unit(row + shape.head + static_cast<int64_t>(u) * kN)
+                           : make_uint4(0, 0, 0, 0);
   }
   int64_t y = -1;
-  float bad = 0.0f;
-  if (g != 0.0f) {
-    y = a.targets[t];
-    if (y < 0 || y >= a.v) {
-      bad = CUDART_NAN_F;
-      if (threadIdx.x == 0 && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
-    }
-  }
-  const float lse = a.lse[t];
-  const float h = e != 0.0f ? a.entropy[t] : 0.0f;
-  for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) {
-    const float lp = fmaf(to_f32(row[j]), a.scale, -lse);
-    const float p = ex2_approx(lp * kLog2e);
-    const float d = (j == y ? g : 0.0f) - p * fmaf(e, fmaxf(lp, -1e30f) + h, g);
-    put(out + j, a.scale * d + bad);
-  }
-}
-
-// One block per row: log-sum-exp, the teacher's probabilities, the loss, then
-// P·q everywhere and the teacher's entries over it.
-template <typename IT, typename GT>
-__global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const DistillArgs a) {
-  __shared__ float sf[kRowThreads / 32];
-  __shared__ float sp[kDistillMaxK];
-  __shared__ int32_t sid[kDistillMaxK];
-  const int64_t t = blockIdx.x;
-  const IT* row = static_cast<const IT*>(a.logits) + t * a.v;
-  auto add = [](float p, float q) { return p + q; };
-  auto max2 = [](float p, float q) { return fmaxf(p, q); };
-  float m = -CUDART_INF_F;
-  for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) m = fmaxf(m, to_f32(row[j]));
-  m = block_reduce(m, sf, max2);
-  if (m == -CUDART_INF_F) m = 0.0f;
-  const float sl = a.scale * kLog2e;
-  float s = 0.0f;
-  for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads)
-    s += ex2_approx((to_f32(row[j]) - m) * sl);
-  s = block_reduce(s, sf, add);
-  const float log_s = logf(s);
-  // the teacher's slots, one per thread
-  const float w = a.weight ? a.weight[t] : 1.0f;
-  int32_t id = -1;
-  float tl = -CUDART_INF_F;
-  if (threadIdx.x < a.K) {
-    id = a.ids[t * a.K + threadIdx.x];
-    if (id != -1) tl = a.teacher[t * a.K + threadIdx.x];
-  }
-  const bool bad = id < -1 || id >= a.v;
-  const float any_bad = block_reduce(bad ? 1.0f : 0.0f, sf, max2);
-  if (bad) tl = -CUDART_INF_F;
-  float tm = 0.0f, log_ts = 0.0f;
-  if (a.renormalize) {
-    tm = block_reduce(tl, sf, max2);
-    if (tm == -CUDART_INF_F) tm = 0.0f;
-    const float ts = block_reduce(expf(tl - tm), sf, add);
-    log_ts = ts == 0.0f ? 0.0f : logf(ts);
-  }
-  const float lp = tl - tm - log_ts;
-  const float p = id == -1 || bad ? 0.0f : expf(lp);
-  const float P = block_reduce(p, sf, add);
-  float term = 0.0f, xk = 0.0f;
-  if (p != 0.0f) {
-    xk = to_f32(row[id]);
-    term = p * (lp - fmaf(a.scale, xk - m, -log_s));
-  }
-  const float loss = block_reduce(term, sf, add);
-  const bool dead = w == 0.0f || (P == 0.0f && any_bad == 0.0f);
-  const bool invalid = !dead && any_bad != 0.0f;
-  if (threadIdx.x == 0) {
-    a.loss[t] = dead ? 0.0f : invalid ? CUDART_NAN_F : w * loss;
-    if (a.lse) a.lse[t] = fmaf(a.scale, m, log_s);
-    if (invalid && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
-  }
-  if (!a.dlogits) return;
-  if (threadIdx.x < a.K) {
-    sid[threadIdx.x] = id;
-    sp[threadIdx.x] = p;
-  }
-  __syncthreads();
-  GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
-  const float c = a.grad_scale * w * a.scale;
-  const float f = invalid ? CUDART_NAN_F : c;
-  float patch = 0.0f;
-  bool first = threadIdx.x < a.K && id >= 0 && !bad;
-  if (first) {
-    float sum = 0.0f;
-    for (int k = 0; k < a.K; ++k)
-      if (sid[k] == id) {
-        if (k < static_cast<int>(threadIdx.x)) first = false;
-        sum += sp[k];
+  float bad = 0.0f, lse = 0.0f, h = 0.0f;
+  if (!zero) {
+    if (g != 0.0f) {
+      y = a.targets[t];
+      if (y < 0 || y >= a.v) {
+        bad = CUDART_NAN_F;
+        if (part == 0 && tid == 0 && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
       }
-    patch = P * ex2_approx((to_f32(row[id]) - m) * sl) / s - sum;
+    }
+    lse = a.lse[t];
+    if (e != 0.0f) h = a.entropy[t];
   }
-  __syncthreads();
-  for (int64_t j = threadIdx.x; j < a.v; j += kRowThreads) {
-    const float q = ex2_approx((to_f32(row[j]) - m) * sl) / s;
-    put(out + j, dead ? 0.0f : f * (P * q));
+  const float geh = fmaf(e, h, g);
+  // scale·(g·[j = y] − p·(g + e·(lp + h))), lp = scale·x − lse, p = exp(lp)
+  auto grad = [&](float x, bool at_y) {
+    const float lp = fmaf(x, a.scale, -lse);
+    const float p = ex2_approx(lp * kLog2e);
+    const float d = (at_y ? g : 0.0f) - p * fmaf(e, max_nan(lp, kLowest), geh);
+    return zero ? 0.0f : fmaf(a.scale, d, bad);
+  };
+#pragma unroll
+  for (int i = 0; i < kBwdUnits; ++i) {
+    const int u = u0 + i * kThreads + tid;
+    if (u >= u1) break;
+    const int64_t j0 = shape.head + static_cast<int64_t>(u) * kN;
+    const int at = static_cast<int>(min(max(y - j0, static_cast<int64_t>(-1)), static_cast<int64_t>(kN)));
+    float x[kN];
+    Unit<IT>::unpack(w[i], x);
+#pragma unroll
+    for (int q = 0; q < kN; ++q) x[q] = grad(x[q], q == at);
+    put_unit<kN>(out + j0, x);
   }
-  __syncthreads();
-  if (first && !dead) put(out + id, f * patch);
+  auto edge = [&](int64_t j) { put(out + j, grad(zero ? 0.0f : to_f32(row[j]), j == y)); };
+  if (part == 0 && tid < shape.head) edge(tid);
+  if (part == blocks - 1 && tid >= 32 && tid < 32 + shape.tail)
+    edge(shape.head + static_cast<int64_t>(shape.units) * kN + tid - 32);
 }
 
 // Combine of the per-slice statistics of the output-layer GEMM (slice k of
@@ -300,47 +636,67 @@ tp_status last_error() { return cudaGetLastError() == cudaSuccess ? TP_OK : TP_E
 
 }  // namespace
 
-tp_status logprobs_fwd_launch(const LogprobsArgs& a, tp_dtype dt, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(a.T);
-  if (dt == TP_DTYPE_BF16)
-    logprobs_row_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(a);
-  else
-    logprobs_row_kernel<float><<<grid, kRowThreads, 0, stream>>>(a);
+namespace {
+
+template <typename IT, bool kTop>
+tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
+  // Blocks per row: one once the rows alone fill the GPU's resident blocks,
+  // else up to eight (the portable cluster size) while each keeps a step or
+  // more of the row.
+  const int64_t units = a.v / Unit<IT>::kN;
+  int slices = 1;
+  while (slices < 8 && a.T * slices * 2 <= 4 * num_sms() && units / (slices * 2) >= 2 * kThreads)
+    slices *= 2;
+  constexpr size_t smem = kTop ? sizeof(Candidates<kThreads * 2 * Unit<IT>::kN>) : 0;
+  static_assert(smem <= 48 * 1024, "within the default limit of dynamic shared memory");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.T * slices));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(slices);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = slices > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, logprobs_kernel<IT, kTop>, a, slices) != cudaSuccess) {
+    cudaGetLastError();
+    return TP_ERR_CUDA;
+  }
+  note_launches(1);
+  return TP_OK;
+}
+
+template <typename IT, typename GT>
+tp_status logprobs_bwd_launch_t(const LogprobsBwdArgs& a, cudaStream_t stream) {
+  const int64_t units = a.v / Unit<IT>::kN;
+  const int64_t blocks = units > 0 ? (units + kThreads * kBwdUnits - 1) / (kThreads * kBwdUnits) : 1;
+  if (a.T * blocks > 0x7fffffff) return TP_ERR_UNSUPPORTED;   // more logits than any GPU holds
+  logprobs_bwd_kernel<IT, GT><<<static_cast<unsigned>(a.T * blocks), kThreads, 0, stream>>>(
+      a, static_cast<int>(blocks));
   note_launches(1);
   return last_error();
+}
+
+}  // namespace
+
+tp_status logprobs_fwd_launch(const LogprobsArgs& a, tp_dtype dt, cudaStream_t stream) {
+  if (dt == TP_DTYPE_BF16)
+    return a.top_k ? logprobs_fwd_launch_t<__nv_bfloat16, true>(a, stream)
+                   : logprobs_fwd_launch_t<__nv_bfloat16, false>(a, stream);
+  return a.top_k ? logprobs_fwd_launch_t<float, true>(a, stream)
+                 : logprobs_fwd_launch_t<float, false>(a, stream);
 }
 
 tp_status logprobs_bwd_launch(const LogprobsBwdArgs& a, tp_dtype dt, tp_dtype grad_dt,
                               cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(a.T);
-  const bool ib = dt == TP_DTYPE_BF16, gb = grad_dt == TP_DTYPE_BF16;
-  if (ib && gb)
-    logprobs_bwd_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(a);
-  else if (ib)
-    logprobs_bwd_kernel<__nv_bfloat16, float><<<grid, kRowThreads, 0, stream>>>(a);
-  else if (gb)
-    logprobs_bwd_kernel<float, __nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(a);
-  else
-    logprobs_bwd_kernel<float, float><<<grid, kRowThreads, 0, stream>>>(a);
-  note_launches(1);
-  return last_error();
-}
-
-tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, float* loss_sum,
-                         cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(a.T);
-  const bool ib = dt == TP_DTYPE_BF16, gb = grad_dt == TP_DTYPE_BF16;
-  if (ib && gb)
-    distill_row_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(a);
-  else if (ib)
-    distill_row_kernel<__nv_bfloat16, float><<<grid, kRowThreads, 0, stream>>>(a);
-  else if (gb)
-    distill_row_kernel<float, __nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(a);
-  else
-    distill_row_kernel<float, float><<<grid, kRowThreads, 0, stream>>>(a);
-  note_launches(1);
-  if (tp_status st = last_error()) return st;
-  return loss_sum ? loss_sum_launch(a.loss, a.T, loss_sum, stream) : TP_OK;
+  if (dt == TP_DTYPE_BF16)
+    return grad_dt == TP_DTYPE_BF16 ? logprobs_bwd_launch_t<__nv_bfloat16, __nv_bfloat16>(a, stream)
+                                    : logprobs_bwd_launch_t<__nv_bfloat16, float>(a, stream);
+  return grad_dt == TP_DTYPE_BF16 ? logprobs_bwd_launch_t<float, __nv_bfloat16>(a, stream)
+                                  : logprobs_bwd_launch_t<float, float>(a, stream);
 }
 
 tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_s,
