@@ -639,14 +639,18 @@ TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t*
  *   temperature beforehand.)  A token listed twice counts twice.
  *
  *   logits [T,v] bf16 or fp32 (dt), dlogits grad_dt, both 16-byte aligned,
- *   any v; dlogits may be the logits themselves when grad_dt == dt and must
- *   not overlap them otherwise.  1 <= K <= 256 (TP_ERR_UNSUPPORTED above).
- *   scale finite and > 0.  v % N == 0; no output depends on N.
+ *   rows of any length up to 1835008 bytes (458752 fp32 or 917504 bf16
+ *   logits: a row is held in the shared memory of eight SMs); dlogits may be
+ *   the logits themselves when grad_dt == dt and must not overlap them
+ *   otherwise.  1 <= K <= 256.  Longer rows and larger K return
+ *   TP_ERR_UNSUPPORTED.  scale finite and > 0.  v % N == 0; no output depends on N.
  *   A row with w == 0, or without a filled slot of probability above 0, has
  *   loss 0 and a gradient of zeros, whatever its logits.  An id outside
  *   [−1, v) in any other row sets TP_DEVERR_RANGE and makes that row's loss
  *   and gradient NaN.  A listed token of probability above 0 whose logit is
- *   −inf gives loss +inf.
+ *   −inf gives loss +inf.  Waits for copies and for the other blocks of a
+ *   row are bounded: if one runs out, TP_DEVERR_TIMEOUT is set and outputs
+ *   are garbage.
  */
 TP_API tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids,
                             const float* teacher_logits, const float* weight, int64_t T,

@@ -856,7 +856,7 @@ tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids
   if (!logits || !teacher_ids || !teacher_logits || !loss) return TP_ERR_NULL;
   if (!dtype_ok(dt) || (dlogits && !dtype_ok(grad_dt))) return TP_ERR_DTYPE;
   if (!dims_ok({T, v, K}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
-  if (K > kDistillMaxK) return TP_ERR_UNSUPPORTED;
+  if (K > kDistillMaxK || v * elem_bytes(dt) > 8 * kDistillMaxSlice) return TP_ERR_UNSUPPORTED;
   if (!ptrs_aligned({logits, dlogits}) ||
       !words_aligned({teacher_ids, teacher_logits, weight, loss, loss_sum, lse}, 4))
     return TP_ERR_ALIGN;
