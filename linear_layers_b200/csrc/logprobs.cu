@@ -55,20 +55,29 @@ __device__ __forceinline__ uint64_t warp_rth_key(uint64_t key, int r) {
   return best;
 }
 
-// Candidates for the row's top k in shared memory, more than enough of them:
-// every element at or above a threshold that at least k elements reach.  The
-// threshold is the smallest over the warps of the ceil(k/8)-th largest of the
-// lanes' maxima.  When more than kLimit candidates have gathered, the
-// threshold is raised among them and the rest dropped; the buffer has room
-// for kLimit and one more step of the whole block, so it cannot overflow.
+// The row's top k, exactly, from one streaming pass.  While a block adds up
+// its range it only notes the maximum of each thread's elements in each of
+// (up to) kGroups stretches of the range.  Then
+//   - the threshold: the smallest over the warps of the ceil(k/8)-th largest
+//     of the lanes' maxima, a key that at least k elements reach;
+//   - the groups whose maximum reaches it (about 1.5·k of them) are read again
+//     from L2 and their elements at or above the threshold become candidates;
+//   - if more than kLimit candidates have gathered (equal or ordered values),
+//     the threshold is raised among them and the rest dropped.  The buffer has
+//     room for kLimit and one more step of the whole block: it cannot overflow.
+// Gathering while streaming instead, against a threshold from the first
+// elements, cost 33 instructions per element of a v=50304 row at k = 64.
 template <int kStep>
 struct Candidates {
   static constexpr int kLimit = 512;
   static constexpr int kRoom = kLimit + kStep + 16;
+  static constexpr int kGroups = 16;
   uint64_t key[kRoom];
   uint64_t warp_key[kWarps];
   uint64_t kth;
-  int n, kept;
+  float group_max[kGroups][kThreads];
+  uint16_t hit[kGroups * kThreads];
+  int n, kept, hits;
 
   // Smallest over the warps of the r-th largest key held by their lanes.
   __device__ __forceinline__ uint64_t threshold(uint64_t lane_key, int k) {
@@ -138,8 +147,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
     logprobs_kernel(const LogprobsArgs a, int slices) {
   constexpr int kN = Unit<IT>::kN;
   constexpr int kUnits = 2;                       // units per thread and step
-  constexpr int kStep = kThreads * kUnits * kN;   // elements per step
-  using Cand = Candidates<kTop ? kStep : 0>;
+  using Cand = Candidates<kTop ? kThreads * kN : 0>;
   extern __shared__ __align__(16) uint8_t dyn_smem[];
   Cand& cand = *reinterpret_cast<Cand*>(dyn_smem);   // only touched with kTop
   __shared__ Sums wsum[kWarps];
@@ -176,26 +184,19 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
       w[i] = u < u1 ? ld_unit(body + static_cast<int64_t>(u) * kN) : fill;
     }
   };
+  // position in the row of unit u's first element
+  auto first_of = [&](int u) { return static_cast<uint32_t>(shape.head + u * kN); };
 
   RowSums sums;
-  [[maybe_unused]] uint64_t floor_key = 0;           // threshold of the candidates
-  [[maybe_unused]] float floor_x = CUDART_NAN_F;     // its value; NaN admits everything
-  [[maybe_unused]] bool full = false;                // a candidate landed at or past kLimit
-  auto admit = [&](uint64_t q) {
-    if constexpr (kTop) {
-      const int at = atomicAdd(&cand.n, 1);
-      cand.key[at] = q;
-      full |= at >= Cand::kLimit;
-    }
-  };
-
   uint4 next[kUnits];
   load(u0, next);
-  if constexpr (kTop) {
-    if (tid == 0) cand.n = 0;
-    __syncthreads();
-  }
   const int steps = (u1 - u0 + kThreads * kUnits - 1) / (kThreads * kUnits);
+  // steps per group, the group being filled, the lane's maximum and the last
+  // position it can have (equal maxima: the first step's)
+  [[maybe_unused]] const int group_steps = (steps + Cand::kGroups - 1) / Cand::kGroups;
+  [[maybe_unused]] int group = 0, group_left = group_steps, lane_step = 0;
+  [[maybe_unused]] float group_mx = -CUDART_INF_F, lane_mx = -CUDART_INF_F;
+  [[maybe_unused]] bool lane_has = false;
   for (int st = 0; st < steps; ++st) {
     const int base = u0 + st * kThreads * kUnits;
     float x[kUnits * kN];
@@ -204,61 +205,96 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
     if (st + 1 < steps) load(base + kThreads * kUnits, next);
     const float mx = sums.add<kUnits * kN, true>(x, sl, tau);
     if constexpr (kTop) {
-      auto index = [&](int i) {   // within the row
-        return static_cast<uint32_t>(shape.head + (base + (i / kN) * kThreads + tid) * kN + i % kN);
-      };
-      auto inside = [&](int i) { return base + (i / kN) * kThreads + tid < u1; };
-      if (st == 0) {
-        // first threshold, from the lanes' maxima of this step
-        uint64_t lane_key = 0;
+      if (st == 0) lane_has = u0 + tid < u1 && x[0] == x[0];
+      if (mx > lane_mx) {
+        lane_mx = mx;
+        lane_step = st;
+      }
+      group_mx = fmaxf(group_mx, mx);
+      if (--group_left == 0 || st + 1 == steps) {
+        cand.group_max[group++][tid] = group_mx;
+        group_mx = -CUDART_INF_F;
+        group_left = group_steps;
+      }
+    }
+  }
+  // the edges of the row: at most kN − 1 elements at each end
+  int edge_j = -1;
+  float edge_x = 0.0f;
+  if (rank == 0 && tid < shape.head) edge_j = tid;
+  if (rank == slices - 1 && tid >= 32 && tid < 32 + shape.tail)
+    edge_j = static_cast<int>(first_of(shape.units)) + tid - 32;
+  if (edge_j >= 0) {
+    edge_x = to_f32(row[edge_j]);
+    sums.add1<true>(edge_x, sl, tau);
+  }
+
+  if constexpr (kTop) {
+    bool full = false;   // a candidate landed at or past kLimit
+    auto admit = [&](uint64_t q) {
+      const int at = atomicAdd(&cand.n, 1);
+      cand.key[at] = q;
+      full |= at >= Cand::kLimit;
+    };
+    if (tid == 0) cand.n = cand.hits = 0;
+    // A lane's key may place its maximum too late, never too early.  A lane
+    // of nothing but −inf (or NaN) has its first element, if that is −inf.
+    uint64_t lane_key = 0;
+    if (lane_mx > -CUDART_INF_F)
+      lane_key = rank_key(lane_mx, first_of(u0 + (lane_step * kUnits + kUnits - 1) * kThreads + tid) + kN - 1);
+    else if (lane_has)
+      lane_key = rank_key(-CUDART_INF_F, first_of(u0 + tid));
+    uint64_t floor_key = cand.threshold(lane_key, a.top_k);   // a barrier within
+    for (int g = 0; g < group; ++g) {
+      const uint32_t at = first_of(u0 + g * group_steps * kUnits * kThreads + tid);
+      if (rank_key(cand.group_max[g][tid], at) >= floor_key)
+        cand.hit[atomicAdd(&cand.hits, 1)] = static_cast<uint16_t>(g * kThreads + tid);
+    }
+    if (edge_j >= 0 && edge_x == edge_x) {
+      const uint64_t q = rank_key(edge_x, static_cast<uint32_t>(edge_j));
+      if (q >= floor_key) admit(q);
+    }
+    __syncthreads();
+    // one unit of a hit group per thread and round
+    const int group_units = group_steps * kUnits;
+    const int items = cand.hits * group_units;
+    for (int base = 0; base < items; base += kThreads) {
+      const int item = base + tid;
+      if (item < items) {
+        const int h = cand.hit[item / group_units];
+        const int u = u0 + ((h / kThreads) * group_units + item % group_units) * kThreads +
+                      h % kThreads;
+        if (u < u1) {
+          float x[kN];
+          Unit<IT>::unpack(*reinterpret_cast<const uint4*>(body + static_cast<int64_t>(u) * kN), x);
+          const float floor_x = floor_key ? key_value(floor_key) : -CUDART_INF_F;
 #pragma unroll
-        for (int i = kUnits * kN - 1; i >= 0; --i)
-          if (x[i] == mx && inside(i)) lane_key = rank_key(mx, index(i));
-        floor_key = cand.threshold(lane_key, a.top_k);
-        floor_x = floor_key ? key_value(floor_key) : CUDART_NAN_F;
-#pragma unroll
-        for (int i = 0; i < kUnits * kN; ++i)
-          if (!(x[i] < floor_x) && x[i] == x[i] && inside(i)) {
-            const uint64_t q = rank_key(x[i], index(i));
-            if (q >= floor_key) admit(q);
-          }
-      } else if (!(mx <= floor_x)) {
-        // later elements equal to the threshold's value come behind it
-#pragma unroll
-        for (int i = 0; i < kUnits * kN; ++i)
-          if (!(x[i] <= floor_x) && x[i] == x[i] && inside(i)) admit(rank_key(x[i], index(i)));
+          for (int i = 0; i < kN; ++i)
+            if (x[i] >= floor_x) {   // not NaN
+              const uint64_t q = rank_key(x[i], first_of(u) + i);
+              if (q >= floor_key) admit(q);
+            }
+        }
       }
       if (__syncthreads_or(full)) {
         int left = cand.shrink(cand.n, a.top_k, floor_key);
         if (left > Cand::kLimit / 2) left = cand.shrink_exact(left, a.top_k, floor_key);
-        floor_x = floor_key ? key_value(floor_key) : CUDART_NAN_F;
         full = false;
         if (tid == 0) cand.n = left;
         __syncthreads();
       }
     }
   }
-  // the edges of the row: at most kN − 1 elements at each end
-  auto edge = [&](int j) {
-    const float x = to_f32(row[j]);
-    sums.add1<true>(x, sl, tau);
-    if constexpr (kTop) {
-      const uint64_t q = x == x ? rank_key(x, static_cast<uint32_t>(j)) : 0;
-      if (q >= floor_key && q) admit(q);
-    }
-  };
-  if (rank == 0 && tid < shape.head) edge(tid);
-  if (rank == slices - 1 && tid >= 32 && tid < 32 + shape.tail)
-    edge(shape.head + shape.units * kN + tid - 32);
 
   const Sums w = warp_sums(sums, sl);
   if ((tid & 31) == 0) wsum[tid >> 5] = w;
   __syncthreads();
-  Sums all = join_sums(kWarps, sl, [&](int i) { return wsum[i]; });
+  Sums all = join_sums(kWarps, wsum[min(tid & 31, kWarps - 1)], sl);
 
   // this block's best: a count of the candidates, rank by rank
   [[maybe_unused]] auto ranked = [&](int n, auto&& out) {
     if constexpr (kTop) {
+      uint64_t floor_key = 0;
       if (n > 2 * a.top_k + 64) n = cand.shrink(n, a.top_k, floor_key);
       for (int i = tid; i < n; i += kThreads) {
         const uint64_t q = cand.key[i];
@@ -274,14 +310,13 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
     if (tid == 0) bsum = all;
     cluster_sync_all();
     if (rank == 0) {
-      all = join_sums(slices, sl, [&](int i) {
-        const uint32_t at = mapa_shared(&bsum, static_cast<uint32_t>(i));
-        Sums q;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.m) : "r"(at));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(at + 4));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.u) : "r"(at + 8));
-        return q;
-      });
+      const uint32_t at =
+          mapa_shared(&bsum, static_cast<uint32_t>(min(tid & 31, slices - 1)));
+      Sums q;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.m) : "r"(at));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(at + 4));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.u) : "r"(at + 8));
+      all = join_sums(slices, q, sl);
       if constexpr (kTop) {
         if (tid == 0) cand.n = 0;
         __syncthreads();
@@ -290,9 +325,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
           asm volatile("ld.shared::cluster.u64 %0, [%1];"
                        : "=l"(q)
                        : "r"(mapa_shared(&best[i % a.top_k], static_cast<uint32_t>(i / a.top_k))));
-          if (q) admit(q);
+          if (q) cand.key[atomicAdd(&cand.n, 1)] = q;   // at most 8·128 of them
         }
-        floor_key = 0;
         __syncthreads();
       }
     }
@@ -469,7 +503,7 @@ tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
   int slices = 1;
   while (slices < 8 && a.T * slices * 2 <= 4 * num_sms() && units / (slices * 2) >= 2 * kThreads)
     slices *= 2;
-  constexpr size_t smem = kTop ? sizeof(Candidates<kThreads * 2 * Unit<IT>::kN>) : 0;
+  constexpr size_t smem = kTop ? sizeof(Candidates<kThreads * Unit<IT>::kN>) : 0;
   static_assert(smem <= 48 * 1024, "within the default limit of dynamic shared memory");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T * slices));

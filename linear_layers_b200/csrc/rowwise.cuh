@@ -4,7 +4,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <math_constants.h>
 
 #include <cmath>
 #include <cstdint>
@@ -125,7 +124,7 @@ struct RowSums {
 #pragma unroll
     for (int i = 4; i < N; i += 4) mx = max3f(max3f(mx, x[i], x[i + 1]), x[i + 2], x[i + 3]);
     if (mx > above) {
-      const float dm = above == -CUDART_INF_F ? 0.0f : max_nan(ref - mx, kLowest);
+      const float dm = above == -INFINITY ? 0.0f : max_nan(ref - mx, kLowest);
       const float al = ex2_approx(dm * sl);
       if (kEntropy)
         u = make_float2(al * fmaf(dm, s.x, u.x), al * fmaf(dm, s.y, u.y));
@@ -148,7 +147,7 @@ struct RowSums {
   // one element (the row's edges)
   template <bool kEntropy>
   __device__ __forceinline__ void add1(float x, float sl, float tau) {
-    const float q[4] = {x, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+    const float q[4] = {x, -INFINITY, -INFINITY, -INFINITY};
     add<4, kEntropy>(q, sl, tau);
   }
 };
@@ -159,14 +158,16 @@ struct Sums {
   float m, s, u;
 };
 
-__device__ __forceinline__ Sums warp_sums(const RowSums& r, float sl) {
-  Sums a{r.above == -CUDART_INF_F ? -CUDART_INF_F : r.ref, r.s.x + r.s.y, r.u.x + r.u.y};
-  float m = a.m;
+// The sum of n <= 32 sums, lane i bringing the i-th (any value past n): the
+// shuffles of a whole warp, the same order and result in every caller.
+__device__ __forceinline__ Sums join_sums(int n, Sums q, float sl) {
+  if (static_cast<int>(threadIdx.x & 31) >= n) q = Sums{-INFINITY, 0.0f, 0.0f};
+  float m = q.m;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  const float d = max_nan(a.m - (m == -CUDART_INF_F ? 0.0f : m), kLowest);
+  const float d = max_nan(q.m - (m == -INFINITY ? 0.0f : m), kLowest);
   const float f = ex2_approx(d * sl);
-  float s = a.s * f, u = f * fmaf(d, a.s, a.u);
+  float s = q.s * f, u = f * fmaf(d, q.s, q.u);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -175,21 +176,11 @@ __device__ __forceinline__ Sums warp_sums(const RowSums& r, float sl) {
   return Sums{m, s, u};
 }
 
-// n sums in order, the same in every caller
-template <typename F>
-__device__ __forceinline__ Sums join_sums(int n, float sl, F get) {
-  float m = -CUDART_INF_F;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, get(i).m);
-  const float r = m == -CUDART_INF_F ? 0.0f : m;
-  float s = 0.0f, u = 0.0f;
-  for (int i = 0; i < n; ++i) {
-    const Sums q = get(i);
-    const float d = max_nan(q.m - r, kLowest);
-    const float f = ex2_approx(d * sl);
-    s = fmaf(q.s, f, s);
-    u = fmaf(f, fmaf(d, q.s, q.u), u);
-  }
-  return Sums{m, s, u};
+// The sums of a warp's threads, on a common reference.
+__device__ __forceinline__ Sums warp_sums(const RowSums& r, float sl) {
+  return join_sums(32,
+                   Sums{r.above == -INFINITY ? -INFINITY : r.ref, r.s.x + r.s.y, r.u.x + r.u.y},
+                   sl);
 }
 
 }  // namespace tpl
