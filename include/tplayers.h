@@ -639,7 +639,7 @@ TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t*
  *   temperature beforehand.)  A token listed twice counts twice.
  *
  *   logits [T,v] bf16 or fp32 (dt), dlogits grad_dt, both 16-byte aligned,
- *   rows of any length up to 1802240 bytes (450560 fp32 or 901120 bf16
+ *   rows of any length up to 1736704 bytes (434176 fp32 or 868352 bf16
  *   logits: a row is held in the shared memory of eight SMs); dlogits may be
  *   the logits themselves when grad_dt == dt and must not overlap them
  *   otherwise.  1 <= K <= 256.  Longer rows and larger K return

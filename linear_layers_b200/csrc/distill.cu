@@ -29,7 +29,9 @@ namespace {
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxSlices = 8;
-constexpr int kSlots = kDistillMaxK / 32;   // teacher slots per lane
+constexpr int kSeenWords = 1024;            // 32768 bits to notice a token listed twice
+constexpr int kChunkUnits = 2048;           // 32 KB of a slice, the grain of its refill
+constexpr int kMaxChunks = static_cast<int>((kDistillMaxSlice + 16 * kChunkUnits - 1) / (16 * kChunkUnits));
 
 // 1-D bulk copy global -> this CTA's shared memory, completion counted in
 // bytes on `bar` (16-byte aligned addresses, size a multiple of 16).
@@ -41,6 +43,13 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
       "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+
+// 4 bytes global -> shared, waited for by the same thread.
+__device__ __forceinline__ void copy_word(void* smem_dst, const void* gsrc) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gsrc)
+               : "memory");
+}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -55,38 +64,42 @@ __device__ __forceinline__ float warp_max(float x) {
 
 // A block's list of the listed tokens that lie in its slice, one for the row
 // at hand and one for the next: id −1 where an earlier entry names the same
-// token, p the token's summed probability (later the gradient written there).
+// token, p the token's summed probability.
 struct SlotLists {
   int32_t* id[2];
   float* p[2];
-  int32_t* raw_id;
-  float* raw_p;
+  float* x;        // the tokens' logits, of the row at hand
+  int32_t* raw_id; // all slots of the next row
+  float* raw_t;
+  uint32_t* seen;  // [kSeenWords], zero between rows
 };
 
 // Persistent clusters of `slices` blocks; cluster c handles rows c, c + C, …
-// Block r of a cluster owns units [r·per, (r+1)·per) of each row, staged by
-// bulk copies `nbuf` rows ahead, block 0 also the row's edges.  The last warp
-// of a block looks after the teacher, the others stream.  Per row:
-//   1. every streaming thread adds up its units;  block barrier
+// Block r of a cluster owns units [r·per, (r+1)·per) of each row, block 0 also
+// the row's edges.  The slice lies in shared memory in chunks; a chunk is
+// refilled with the next row's as soon as its gradient is written, so reads
+// of one row run beside the writes of the one before.  Of a block's warps the
+// last issues the copies, the one before looks after the teacher, the others
+// stream.  Per row:
+//   1. every streaming thread adds up its units as the chunks arrive;  barrier
 //   2. the teacher warp adds A and P of the block's own tokens and sends
 //      (r, S, A, P) to every block of the cluster, one 16-byte asynchronous
 //      store counted on the receiver's barrier; then it turns the next row's
 //      slots (loaded a row ahead) into probabilities;
 //   3. the blocks combine the records in slice order and the streaming
-//      threads write P·q over their slice;  block barrier
-//   4. the teacher warp writes the listed tokens over that, and the buffer is
-//      refilled.
+//      threads write P·q over their slice, handing back chunk by chunk;
+//   4. the teacher warp, behind a barrier, writes the listed tokens over that.
 template <typename IT, typename GT>
-__global__ void __launch_bounds__(kMaxThreads + 32, 1)
-    distill_kernel(const DistillArgs a, int slices, int per, int nbuf, uint32_t buf_stride,
-                   uint64_t wait_ns) {
+__global__ void __launch_bounds__(kMaxThreads + 64, 2)
+    distill_kernel(const DistillArgs a, int slices, int per, uint32_t buf_bytes, uint64_t wait_ns) {
   constexpr int kN = Unit<IT>::kN;
-  extern __shared__ __align__(128) uint8_t buffers[];     // the slices, then the slot lists
+  extern __shared__ __align__(128) uint8_t buffer[];      // the slice, then the slot lists
   __shared__ __align__(16) float rec[2][kMaxSlices][4];   // [row parity][slice] (r, S, A, P)
   __shared__ __align__(8) uint64_t rec_bar[2];
-  __shared__ __align__(8) uint64_t load_bar[2];
-  __shared__ Sums wsum[kMaxWarps];
-  __shared__ float edge[2][8];             // the row's edges (block 0)
+  __shared__ __align__(8) uint64_t full[kMaxChunks];      // a chunk of the row has landed
+  __shared__ __align__(8) uint64_t empty[kMaxChunks];     // ... and nothing reads it any more
+  __shared__ Sums wsum[2][kMaxWarps];
+  __shared__ float edge[2][2][8];          // [row parity] the row's two edges (block 0)
   __shared__ float teacher_p[2], teacher_c[2];
   __shared__ int teacher_bad[2];
 
@@ -94,56 +107,79 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
   const int64_t cluster = blockIdx.x / static_cast<unsigned>(slices);
   const int64_t clusters = gridDim.x / static_cast<unsigned>(slices);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int threads = static_cast<int>(blockDim.x) - 32, warps = threads >> 5;
+  const int threads = static_cast<int>(blockDim.x) - 64, warps = threads >> 5;
+  const int chunks = (per + kChunkUnits - 1) / kChunkUnits;
   const float sl = a.scale * kLog2e, tau = 8.0f / sl;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&rec_bar[i], 1);
-      mbar_init(&load_bar[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&rec_bar[i], 1);
+    for (int c = 0; c < chunks; ++c) {
+      mbar_init(&full[c], 1);
+      // the streaming warps and, where a gradient may overwrite the logits, the teacher's
+      mbar_init(&empty[c], static_cast<uint32_t>(warps) + (a.dlogits != nullptr ? 1 : 0));
     }
     fence_mbarrier_init();
   }
   __syncthreads();
   if (slices > 1) cluster_sync_all();   // every barrier exists before a peer signals it
 
+  const volatile int never = 0;   // no role of the block cuts another's wait short
   auto timeout = [&]() {
     if (a.dev_status) atomicOr(a.dev_status, TP_DEVERR_TIMEOUT);
   };
   // the row's softmax sums over all slices (every thread of a warp calls it)
   auto row_sums = [&](int k) {
-    if (slices == 1) return join_sums(warps, wsum[min(lane, warps - 1)], sl);
+    if (slices == 1) return join_sums(warps, wsum[k & 1][min(lane, warps - 1)], sl);
     if (!mbar_wait_cluster_bounded(&rec_bar[k & 1], static_cast<uint32_t>(k >> 1) & 1u, wait_ns))
       timeout();
     const float* q = rec[k & 1][min(lane, slices - 1)];
     return join_sums(slices, Sums{q[0], q[1], 0.0f}, sl);
   };
 
-  if (warp == warps) {
+  if (warp == warps + 1) {
+    // ----------------------------------------------------------------- copies
+    if (lane == 0) {
+      int k = 0;
+      for (int64_t t = cluster; t < a.T; t += clusters, ++k) {
+        const RowShape<IT> shape(t * a.v, a.v);
+        const int u0 = min(rank * per, shape.units);
+        const int n = min(u0 + per, shape.units) - u0;
+        const char* src = static_cast<const char*>(a.logits) +
+                          (t * a.v + shape.head) * static_cast<int64_t>(sizeof(IT)) +
+                          static_cast<int64_t>(u0) * 16;
+        for (int c = 0; c < chunks; ++c) {
+          if (k > 0 && !mbar_wait_bounded(&empty[c], static_cast<uint32_t>(k - 1) & 1u, wait_ns, &never))
+            timeout();
+          const int units = min(max(n - c * kChunkUnits, 0), kChunkUnits);
+          mbar_arrive_expect_tx(&full[c], static_cast<uint32_t>(units) * 16u);
+          if (units > 0)
+            bulk_load(buffer + c * kChunkUnits * 16, src + static_cast<int64_t>(c) * kChunkUnits * 16,
+                      static_cast<uint32_t>(units) * 16u, &full[c]);
+        }
+      }
+    }
+  } else if (warp == warps) {
     // ---------------------------------------------------------------- teacher
     SlotLists list;
     {
-      uint8_t* at = buffers + nbuf * buf_stride;
+      uint8_t* at = buffer + buf_bytes;
       const int bytes = a.K * 4;
       for (int i = 0; i < 2; ++i) {
         list.id[i] = reinterpret_cast<int32_t*>(at + 2 * i * bytes);
         list.p[i] = reinterpret_cast<float*>(at + (2 * i + 1) * bytes);
       }
       list.raw_id = reinterpret_cast<int32_t*>(at + 4 * bytes);
-      list.raw_p = reinterpret_cast<float*>(at + 5 * bytes);
+      list.raw_t = reinterpret_cast<float*>(at + 5 * bytes);
+      list.x = reinterpret_cast<float*>(at + 6 * bytes);
+      list.seen = reinterpret_cast<uint32_t*>(at + 7 * bytes);
+      for (int i = lane; i < kSeenWords; i += 32) list.seen[i] = 0;
+      __syncwarp();
     }
-    int32_t next_id[kSlots];   // slot lane + 32·i of the row after the prepared one
-    float next_t[kSlots];
+    // row t's slots on their way into the lists' raw places, lane by lane
     auto fetch = [&](int64_t t) {
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        const int s = lane + 32 * i;
-        next_id[i] = -1;
-        next_t[i] = -CUDART_INF_F;
-        if (s < a.K) {
-          next_id[i] = a.ids[t * a.K + s];
-          next_t[i] = a.teacher[t * a.K + s];
-        }
+      for (int s = lane; s < a.K; s += 32) {
+        copy_word(&list.raw_id[s], a.ids + t * a.K + s);
+        copy_word(&list.raw_t[s], a.teacher + t * a.K + s);
       }
     };
     // probabilities of row t's slots and the list of this block's own; how many
@@ -152,53 +188,49 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
       const int own0 = shape.head + min(rank * per, shape.units) * kN;
       const int own1 = shape.head + min(rank * per + per, shape.units) * kN;
       const int body1 = shape.head + shape.units * kN;
+      copy_wait();
       bool bad = false;
       float top = -CUDART_INF_F;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (32 * i >= a.K) break;
-        const bool out = next_id[i] < -1 || next_id[i] >= a.v;
+      for (int s = lane; s < a.K; s += 32) {
+        const int id = list.raw_id[s];
+        const bool out = id < -1 || id >= a.v;
         bad |= out;
-        if (out || next_id[i] == -1) {   // the value of an empty slot is not looked at
-          next_id[i] = -1;
-          next_t[i] = -CUDART_INF_F;
+        if (out || id == -1) {   // the value of an empty slot is not looked at
+          list.raw_id[s] = -1;
+          list.raw_t[s] = -CUDART_INF_F;
         }
-        top = fmaxf(top, next_t[i]);
+        top = fmaxf(top, list.raw_t[s]);
       }
+      float log_sum = 0.0f;
       if (a.renormalize) {
         top = warp_max(top);
         if (top == -CUDART_INF_F) top = 0.0f;
         float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-          if (32 * i >= a.K) break;
-          next_t[i] -= top;
-          sum += expf(next_t[i]);
-        }
+        for (int s = lane; s < a.K; s += 32) sum += expf(list.raw_t[s] - top);
         sum = warp_sum(sum);
-        const float log_sum = sum == 0.0f ? 0.0f : logf(sum);
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-          if (32 * i >= a.K) break;
-          next_t[i] -= log_sum;
-        }
+        log_sum = sum == 0.0f ? 0.0f : logf(sum);
+      } else {
+        top = 0.0f;
       }
       float P = 0.0f, C = 0.0f;
       int n = 0;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (32 * i >= a.K) break;
-        const int id = next_id[i];
-        const float p = id == -1 ? 0.0f : expf(next_t[i]);
+      for (int s0 = 0; s0 < a.K; s0 += 32) {
+        int id = -1;
+        float lp = 0.0f, p = 0.0f;
+        if (s0 + lane < a.K) {
+          id = list.raw_id[s0 + lane];
+          lp = (list.raw_t[s0 + lane] - top) - log_sum;
+          if (id != -1) p = expf(lp);
+        }
         P += p;
-        if (p != 0.0f) C = fmaf(p, next_t[i], C);
+        if (p != 0.0f) C = fmaf(p, lp, C);
         const bool own = p != 0.0f && ((id >= own0 && id < own1) ||
                                        (rank == 0 && (id < shape.head || id >= body1)));
         const uint32_t mask = __ballot_sync(0xffffffffu, own);
         if (own) {
           const int at = n + __popc(mask & ((1u << lane) - 1u));
-          list.raw_id[at] = id;
-          list.raw_p[at] = p;
+          list.id[b][at] = id;
+          list.p[b][at] = p;
         }
         n += __popc(mask);
       }
@@ -211,17 +243,35 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
         teacher_bad[b] = bad;
       }
       __syncwarp();
-      for (int e = lane; e < n; e += 32) {   // one entry per token, summed in slot order
-        const int id = list.raw_id[e];
-        float sum = 0.0f;
-        bool first = true;
-        for (int q = 0; q < n; ++q)
-          if (list.raw_id[q] == id) {
-            if (q < e) first = false;
-            sum += list.raw_p[q];
-          }
-        list.id[b][e] = first ? id : -1;
-        list.p[b][e] = sum;
+      // A token listed twice shows as a bit of `seen` that was set already;
+      // that it is one, and not two tokens on one bit, is looked up.
+      bool twice = false;
+      for (int e = lane; e < n; e += 32) {
+        const uint32_t bit = static_cast<uint32_t>(list.id[b][e]) & (kSeenWords * 32 - 1);
+        if ((atomicOr(&list.seen[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u)
+          for (int q = 0; q < n; ++q) twice |= q != e && list.id[b][q] == list.id[b][e];
+      }
+      __syncwarp();
+      for (int e = lane; e < n; e += 32)
+        list.seen[(static_cast<uint32_t>(list.id[b][e]) & (kSeenWords * 32 - 1)) >> 5] = 0;
+      if (__any_sync(0xffffffffu, twice)) {   // one entry per token, summed in slot order
+        for (int e = lane; e < n; e += 32) {
+          const int id = list.id[b][e];
+          float sum = 0.0f;
+          bool first = true;
+          for (int q = 0; q < n; ++q)
+            if (list.id[b][q] == id) {
+              if (q < e) first = false;
+              sum += list.p[b][q];
+            }
+          list.raw_id[e] = first ? id : -1;
+          list.raw_t[e] = sum;
+        }
+        __syncwarp();
+        for (int e = lane; e < n; e += 32) {
+          list.id[b][e] = list.raw_id[e];
+          list.p[b][e] = list.raw_t[e];
+        }
       }
       __syncwarp();
       return n;
@@ -235,27 +285,30 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
     }
     int k = 0;
     for (int64_t t = cluster; t < a.T; t += clusters, ++k) {
-      const int par = k & 1, buf = nbuf == 2 ? par : 0;
+      const int par = k & 1;
       const RowShape<IT> shape(t * a.v, a.v);
       const int own0 = shape.head + min(rank * per, shape.units) * kN;
       const int own1 = shape.head + min(rank * per + per, shape.units) * kN;
-      const IT* slice = reinterpret_cast<const IT*>(buffers + buf * buf_stride);
+      const IT* slice = reinterpret_cast<const IT*>(buffer);
       auto value = [&](int j) {
+        if (a.dlogits == nullptr) return to_f32(static_cast<const IT*>(a.logits)[t * a.v + j]);
         if (j >= own0 && j < own1) return to_f32(slice[j - own0]);
-        return j < shape.head ? edge[0][j] : edge[1][j - shape.head - shape.units * kN];
+        return j < shape.head ? edge[par][0][j] : edge[par][1][j - shape.head - shape.units * kN];
       };
       const float w = a.weight ? a.weight[t] : 1.0f;
-      __syncthreads();                          // the block's sums and edges
-      if (!mbar_wait_cluster_bounded(&load_bar[buf],
-                                     static_cast<uint32_t>(nbuf == 2 ? k >> 1 : k) & 1u, wait_ns))
-        timeout();
-      const Sums own = join_sums(warps, wsum[min(lane, warps - 1)], sl);
+      named_barrier_sync(1, static_cast<uint32_t>(threads) + 32);   // the block's sums and edges
+      if (a.dlogits != nullptr)
+        for (int c = 0; c < chunks; ++c)   // landed: the streaming warps have waited for them
+          if (!mbar_wait_bounded(&full[c], static_cast<uint32_t>(k) & 1u, wait_ns, &never)) timeout();
+      const Sums own = join_sums(warps, wsum[par][min(lane, warps - 1)], sl);
       const float own_ref = own.m == -CUDART_INF_F ? 0.0f : own.m;
       float A = 0.0f, Pown = 0.0f;
       for (int e = lane; e < n; e += 32) {
         const int id = list.id[par][e];
         if (id >= 0) {
-          A = fmaf(list.p[par][e], value(id) - own_ref, A);
+          const float x = value(id);
+          list.x[e] = x;
+          A = fmaf(list.p[par][e], x - own_ref, A);
           Pown += list.p[par][e];
         }
       }
@@ -264,6 +317,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
       if (slices > 1 && lane < slices)
         st_async_v4(mapa_shared(&rec[par][rank][0], static_cast<uint32_t>(lane)),
                     mapa_shared(&rec_bar[par], static_cast<uint32_t>(lane)), own.m, own.s, A, Pown);
+      if (a.dlogits != nullptr && lane < chunks) mbar_arrive(&empty[lane]);   // behind the shuffles: every lane has read
       int n_next = 0;
       if (t + clusters < a.T) {
         n_next = prepare(t + clusters, par ^ 1);
@@ -290,50 +344,40 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
           if (!dead && any_bad && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
         }
       }
-      const bool patches = a.dlogits != nullptr && !dead;
-      if (patches) {
-        const float c = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale;
-        const float inv = 1.0f / all.s;
-        for (int e = lane; e < n; e += 32) {
-          const int id = list.id[par][e];
-          if (id >= 0)
-            list.p[par][e] = c * (P * (ex2_approx((value(id) - ref) * sl) * inv) - list.p[par][e]);
-        }
-      }
-      __syncthreads();                          // P·q is written, the slice has been read
-      if (patches) {
-        GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
-        for (int e = lane; e < n; e += 32) {
-          const int id = list.id[par][e];
-          if (id >= 0) put(out + id, list.p[par][e]);
+      if (a.dlogits != nullptr) {
+        named_barrier_sync(2, static_cast<uint32_t>(threads) + 32);   // P·q is written
+        if (!dead) {
+          const float c = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale;
+          const float inv = 1.0f / all.s;
+          GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
+          for (int e = lane; e < n; e += 32) {
+            const int id = list.id[par][e];
+            if (id >= 0)
+              put(out + id, c * (P * (ex2_approx((list.x[e] - ref) * sl) * inv) - list.p[par][e]));
+          }
         }
       }
       n = n_next;
     }
   } else {
     // -------------------------------------------------------------- streaming
-    auto issue = [&](int b, int64_t t) {   // one thread: this block's slice of row t
-      const RowShape<IT> shape(t * a.v, a.v);
-      const int u0 = min(rank * per, shape.units), u1 = min(u0 + per, shape.units);
-      const uint32_t bytes = static_cast<uint32_t>(u1 - u0) * 16u;
-      mbar_arrive_expect_tx(&load_bar[b], bytes);
-      const char* src = static_cast<const char*>(a.logits) +
-                        (t * a.v + shape.head) * static_cast<int64_t>(sizeof(IT)) +
-                        static_cast<int64_t>(u0) * 16;
-      uint8_t* dst = buffers + b * buf_stride;
-      for (uint32_t off = 0; off < bytes; off += 16384u)
-        bulk_load(dst + off, src + off, min(bytes - off, 16384u), &load_bar[b]);
+    const uint4* slice = reinterpret_cast<const uint4*>(buffer);
+    auto release = [&](int c) {   // this warp has read chunk c for the last time
+      __syncwarp();
+      if (lane == 0) {
+        fence_proxy_async_smem();   // the reads come before the refill's writes
+        mbar_arrive(&empty[c]);
+      }
     };
-    if (tid == 0)
-      for (int b = 0; b < nbuf; ++b)
-        if (cluster + b * clusters < a.T) issue(b, cluster + b * clusters);
+    constexpr int kBatch = 16 / kN;   // units a thread has in hand: 16 logits
+    constexpr uint32_t kInf = Unit<IT>::kMinusInf;
+    const uint4 fill = make_uint4(kInf, kInf, kInf, kInf);
     int k = 0;
     for (int64_t t = cluster; t < a.T; t += clusters, ++k) {
-      const int par = k & 1, buf = nbuf == 2 ? par : 0;
+      const int par = k & 1;
       const RowShape<IT> shape(t * a.v, a.v);
       const int u0 = min(rank * per, shape.units);
       const int n = min(u0 + per, shape.units) - u0;
-      const uint4* slice = reinterpret_cast<const uint4*>(buffers + buf * buf_stride);
       const float w = a.weight ? a.weight[t] : 1.0f;
       // this row's records: one arrival here, 16 bytes from each slice
       if (tid == 0 && slices > 1)
@@ -345,70 +389,76 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1)
       float edge_x = 0.0f;
       if (is_head || is_tail) {
         edge_x = to_f32(static_cast<const IT*>(a.logits)[t * a.v + edge_j]);
-        edge[is_head ? 0 : 1][is_head ? tid : tid - 32] = edge_x;
+        edge[par][is_head ? 0 : 1][is_head ? tid : tid - 32] = edge_x;
       }
-      if (!mbar_wait_cluster_bounded(&load_bar[buf],
-                                     static_cast<uint32_t>(nbuf == 2 ? k >> 1 : k) & 1u, wait_ns))
-        timeout();
       RowSums sums;
-      int u = tid;
-      for (; u + threads < n; u += 2 * threads) {
-        float x[2 * kN];
-        Unit<IT>::unpack(slice[u], x);
-        Unit<IT>::unpack(slice[u + threads], x + kN);
-        sums.add<2 * kN, false>(x, sl, tau);
-      }
-      if (u < n) {
-        float x[kN];
-        Unit<IT>::unpack(slice[u], x);
-        sums.add<kN, false>(x, sl, tau);
+      for (int c = 0; c < chunks; ++c) {
+        if (!mbar_wait_bounded(&full[c], static_cast<uint32_t>(k) & 1u, wait_ns, &never)) timeout();
+        const int end = min((c + 1) * kChunkUnits, n);
+        for (int u = c * kChunkUnits + tid; u < end; u += kBatch * threads) {
+          float x[kBatch * kN];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            Unit<IT>::unpack(u + i * threads < end ? slice[u + i * threads] : fill, x + i * kN);
+          sums.add<kBatch * kN, false>(x, sl, tau);
+        }
+        if (a.dlogits == nullptr) release(c);
       }
       if (is_head || is_tail) sums.add1<false>(edge_x, sl, tau);
       const Sums ws = warp_sums(sums, sl);
-      if (lane == 0) wsum[warp] = ws;
-      __syncthreads();
+      if (lane == 0) wsum[par][warp] = ws;
+      named_barrier_sync(1, static_cast<uint32_t>(threads) + 32);
+      if (a.dlogits == nullptr) {
+        if (slices > 1) row_sums(k);   // the records of row k+2 reuse this row's places
+        continue;
+      }
       const Sums all = row_sums(k);
-      if (a.dlogits != nullptr) {
-        const float ref = all.m == -CUDART_INF_F ? 0.0f : all.m;
-        const float P = teacher_p[par];
-        const bool any_bad = teacher_bad[par] != 0;
-        const bool dead = w == 0.0f || (P == 0.0f && !any_bad);
-        const float coef =
-            any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale * (P * (1.0f / all.s));
-        GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
-        GT* dst = out + shape.head + static_cast<int64_t>(u0) * kN;
+      const float ref = all.m == -CUDART_INF_F ? 0.0f : all.m;
+      const float P = teacher_p[par];
+      const bool any_bad = teacher_bad[par] != 0;
+      const bool dead = w == 0.0f || (P == 0.0f && !any_bad);
+      const float coef = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale * (P * (1.0f / all.s));
+      GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
+      GT* dst = out + shape.head + static_cast<int64_t>(u0) * kN;
+      const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
+      const float2 c2 = make_float2(coef, coef);
+      for (int c = 0; c < chunks; ++c) {
+        const int end = min((c + 1) * kChunkUnits, n);
         if (dead) {
           const float z[kN] = {};
-          for (u = tid; u < n; u += threads) put_unit<kN>(dst + static_cast<int64_t>(u) * kN, z);
+          for (int u = c * kChunkUnits + tid; u < end; u += threads)
+            put_unit<kN>(dst + static_cast<int64_t>(u) * kN, z);
         } else {
-          const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
-          const float2 c2 = make_float2(coef, coef);
-#pragma unroll 2
-          for (u = tid; u < n; u += threads) {
-            float x[kN];
-            Unit<IT>::unpack(slice[u], x);
+          for (int u = c * kChunkUnits + tid; u < end; u += kBatch * threads) {
+            uint4 w4[kBatch];
 #pragma unroll
-            for (int i = 0; i < kN; i += 2) {
-              const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), nr), sl2);
-              const float2 g = __fmul2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), c2);
-              x[i] = g.x;
-              x[i + 1] = g.y;
+            for (int i = 0; i < kBatch; ++i)
+              w4[i] = u + i * threads < end ? slice[u + i * threads] : fill;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              float x[kN];
+              Unit<IT>::unpack(w4[i], x);
+#pragma unroll
+              for (int q = 0; q < kN; q += 2) {
+                const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[q], x[q + 1]), nr), sl2);
+                const float2 g = __fmul2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), c2);
+                x[q] = g.x;
+                x[q + 1] = g.y;
+              }
+              if (u + i * threads < end)
+                put_unit<kN>(dst + static_cast<int64_t>(u + i * threads) * kN, x);
             }
-            put_unit<kN>(dst + static_cast<int64_t>(u) * kN, x);
           }
         }
-        if (is_head || is_tail)
-          put(out + edge_j, dead ? 0.0f : coef * ex2_approx((edge_x - ref) * sl));
+        release(c);
       }
-      // every read of this row's slice is done, and the writes of P·q are
-      // ordered before the listed tokens'
-      __syncthreads();
-      if (tid == 0 && t + nbuf * clusters < a.T) {
-        fence_proxy_async_smem();
-        issue(buf, t + nbuf * clusters);
-      }
+      if (is_head || is_tail)
+        put(out + edge_j, dead ? 0.0f : coef * ex2_approx((edge_x - ref) * sl));
+      // the teacher warp's writes come after these; nothing here waits
+      named_barrier_arrive(2, static_cast<uint32_t>(threads) + 32);
     }
   }
+  __syncthreads();
   if (slices > 1) cluster_sync_all();   // every peer's record into this block has landed
 }
 
@@ -416,35 +466,35 @@ template <typename IT, typename GT>
 tp_status distill_launch_t(const DistillArgs& a, cudaStream_t stream) {
   constexpr int64_t kN = Unit<IT>::kN;
   const int64_t units = (a.v + kN - 1) / kN;
-  // Slices of a row: enough that one is at most 26 KB, so that several blocks
-  // share an SM and one's writes run beside another's reads; with few rows,
-  // more of them while each keeps 4 KB.
+  // Slices of a row: at most 108 KB, so that two blocks share an SM and one's
+  // barriers and exchanges run beside the other's sweeps; with few rows, more
+  // of them while each keeps 4 KB.
   int slices = 1;
   while (slices < kMaxSlices &&
-         (units * 16 > 26 * 1024 * slices ||
+         (units * 16 > 108 * 1024 * slices ||
           (a.T * slices * 2 <= num_sms() && units * 16 >= 8192 * slices)))
     slices *= 2;
   if (const char* e = getenv("TPX_SL")) slices = atoi(e);
   const int per = static_cast<int>((units + slices - 1) / slices);
-  const int64_t stride = (static_cast<int64_t>(per) * 16 + 127) & ~int64_t{127};
-  if (stride > kDistillMaxSlice) return TP_ERR_UNSUPPORTED;
-  const int nbuf = 2 * stride <= kDistillMaxSlice ? 2 : 1;
-  int threads = stride <= 32 * 1024 ? 128 : stride <= 56 * 1024 ? 256 : 512;
+  const int64_t slice = (static_cast<int64_t>(per) * 16 + 127) & ~int64_t{127};
+  if (slice > kDistillMaxSlice) return TP_ERR_UNSUPPORTED;
+  int threads = slice <= 16 * 1024 ? 128 : slice <= 50 * 1024 ? 256 : 512;
   if (const char* e = getenv("TPX_NT")) threads = atoi(e);
-  const int smem = static_cast<int>(stride * nbuf + 24 * a.K);   // and the slot lists
+  const int smem = static_cast<int>(slice + 28 * a.K + 4 * kSeenWords);   // and the slot lists
   int dev = 0;
   cudaGetDevice(&dev);
   static bool configured[64] = {false};
   if (!configured[dev & 63]) {
     if (cudaFuncSetAttribute(distill_kernel<IT, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kDistillMaxSlice + 24 * kDistillMaxK)) != cudaSuccess ||
+                             static_cast<int>(kDistillMaxSlice + 28 * kDistillMaxK +
+                                              4 * kSeenWords)) != cudaSuccess ||
         cudaFuncSetAttribute(distill_kernel<IT, GT>, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return TP_ERR_CUDA;
     configured[dev & 63] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(static_cast<unsigned>(threads + 32));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads + 64));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -474,8 +524,8 @@ tp_status distill_launch_t(const DistillArgs& a, cudaStream_t stream) {
   }
   const int64_t clusters = a.T < last.clusters ? a.T : last.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * slices));
-  if (cudaLaunchKernelEx(&cfg, distill_kernel<IT, GT>, a, slices, per, nbuf,
-                         static_cast<uint32_t>(stride), wait_limit_ns()) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, distill_kernel<IT, GT>, a, slices, per,
+                         static_cast<uint32_t>(slice), wait_limit_ns()) != cudaSuccess) {
     cudaGetLastError();
     return TP_ERR_CUDA;
   }

@@ -176,8 +176,8 @@ tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_
 // Distillation from a teacher's top entries: see vp_distill.
 constexpr int kDistillMaxK = 256;
 // Bytes of a block's slices of logits in shared memory; eight blocks hold a
-// row, so a row may have 8·225280 bytes.
-constexpr int64_t kDistillMaxSlice = 220 * 1024;
+// row, so a row may have 8·217088 bytes.
+constexpr int64_t kDistillMaxSlice = 212 * 1024;
 struct DistillArgs {
   const void* logits;
   const int32_t* ids;       // [T, K], -1: empty slot

@@ -454,6 +454,12 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthread
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Arrive without waiting: the barrier's waiting threads see what this thread
+// has written before.
+__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // Barrier over `nthreads` threads that also returns the AND of `pred` over
 // them: every participant leaves with the same answer.
 __device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t nthreads, bool pred) {

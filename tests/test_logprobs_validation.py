@@ -140,7 +140,7 @@ def test_distill_abi(L):
     assert f(dt=3) == f(d=ctypes.c_void_p(1 << 21), gdt=9) == DTYPE
     assert f(K=0) == f(T=0) == f(v=0) == f(N=7) == f(scale=float("nan")) == SHAPE
     assert f(K=257) == UNSUPPORTED and f(d=P) == UNSUPPORTED
-    assert f(v=450562) == UNSUPPORTED and f(v=901122, dt=0) == UNSUPPORTED
+    assert f(v=434178) == UNSUPPORTED and f(v=868354, dt=0) == UNSUPPORTED
     assert f(x=ODD) == f(d=ODD) == ALIGN
 
 
