@@ -99,7 +99,8 @@ typedef enum {
   TP_OP_LINEAR_XENT = 6,  /* pass (T, h, v, N) */
   TP_OP_SP_LN_BWD = 7,    /* pass (M, h, h, N): M token rows of width h */
   TP_OP_ATTENTION_BWD = 8, /* pass (b·s, n_heads, 64, N) */
-  TP_OP_LINEAR_LOGPROBS = 9 /* pass (T, h, v, N) */
+  TP_OP_LINEAR_LOGPROBS = 9, /* pass (T, h, v, N) */
+  TP_OP_DISTILL = 10         /* pass (T, K, v, N) */
 } tp_op;
 
 /*
@@ -639,8 +640,7 @@ TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t*
  *   temperature beforehand.)  A token listed twice counts twice.
  *
  *   logits [T,v] bf16 or fp32 (dt), dlogits grad_dt, both 16-byte aligned,
- *   rows of any length up to 1736704 bytes (434176 fp32 or 868352 bf16
- *   logits: a row is held in the shared memory of eight SMs); dlogits may be
+ *   any v up to 337920 (a row is held on chip by eight SMs); dlogits may be
  *   the logits themselves when grad_dt == dt and must not overlap them
  *   otherwise.  1 <= K <= 256.  Longer rows and larger K return
  *   TP_ERR_UNSUPPORTED.  scale finite and > 0.  v % N == 0; no output depends on N.
@@ -648,7 +648,8 @@ TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t*
  *   loss 0 and a gradient of zeros, whatever its logits.  An id outside
  *   [−1, v) in any other row sets TP_DEVERR_RANGE and makes that row's loss
  *   and gradient NaN.  A listed token of probability above 0 whose logit is
- *   −inf gives loss +inf.  Waits for copies and for the other blocks of a
+ *   −inf gives loss +inf.  ws, ws_bytes >= tp_workspace_bytes(TP_OP_DISTILL,
+ *   T, K, v, N), 16-byte aligned (the merged slots).  Waits for copies and for the other blocks of a
  *   row are bounded: if one runs out, TP_DEVERR_TIMEOUT is set and outputs
  *   are garbage.
  */
@@ -656,7 +657,8 @@ TP_API tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teac
                             const float* teacher_logits, const float* weight, int64_t T,
                             int64_t v, int32_t K, int32_t N, int32_t renormalize, float scale,
                             float grad_scale, float* loss, float* loss_sum, float* lse,
-                            void* dlogits, tp_dtype grad_dt, int32_t* dev_status, void* stream);
+                            void* dlogits, tp_dtype grad_dt, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, void* stream);
 
 /*
  * Output layer and log-probabilities in one pass, without the logits matrix

@@ -34,14 +34,15 @@ __all__ = [
     "tp_attention_fwd", "tp_sp_dropout_add_ln_fwd", "tp_sp_dropout_add_ln_bwd", "OP_SP_LN_BWD",
     "tp_attention_bwd", "OP_ATTENTION_BWD",
     "vp_logprobs_fwd", "vp_logprobs_bwd", "vp_distill",
-    "tp_linear_logprobs_fwd", "tp_linear_logprobs_dlogits", "OP_LINEAR_LOGPROBS",
+    "tp_linear_logprobs_fwd", "tp_linear_logprobs_dlogits", "OP_LINEAR_LOGPROBS", "OP_DISTILL",
     "OP_MLP_FWD", "OP_MLP_BWD", "OP_ROW_LINEAR_FWD", "OP_COL_LINEAR_BWD", "OP_ROW_LINEAR_BWD",
 ]
 
 ACT_NONE, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2
 DTYPE_BF16, DTYPE_F32 = 0, 1
 (OP_MLP_FWD, OP_MLP_BWD, OP_ROW_LINEAR_FWD, OP_COL_LINEAR_BWD, OP_ROW_LINEAR_BWD, OP_EMBED_BWD,
- OP_LINEAR_XENT, OP_SP_LN_BWD, OP_ATTENTION_BWD, OP_LINEAR_LOGPROBS) = range(10)
+ OP_LINEAR_XENT, OP_SP_LN_BWD, OP_ATTENTION_BWD, OP_LINEAR_LOGPROBS,
+ OP_DISTILL) = range(11)
 DEVERR_RANGE, DEVERR_TIMEOUT = 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -94,7 +95,7 @@ _SIGS = {
     "vp_logprobs_bwd": ([_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I32, _F, _P, _I32, _P, _P],
                         _I32),
     "vp_distill": ([_P, _I32, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _F, _F, _P, _P, _P, _P,
-                    _I32, _P, _P], _I32),
+                    _I32, _P, _SZ, _P, _P], _I32),
     "tp_linear_logprobs_fwd": ([_P, _P, _P, _I64, _I64, _I64, _I32, _F, _P, _P, _P, _P, _SZ, _P,
                                 _P], _I32),
     "tp_linear_logprobs_dlogits": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _F, _P,
@@ -764,7 +765,7 @@ def vp_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, N, *, sca
 
 def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weight=None,
                scale=1.0, grad_scale=1.0, with_grad=True, grad_dtype=torch.bfloat16, loss=None,
-               loss_sum=None, lse=None, dlogits=None, dev_status=None):
+               loss_sum=None, lse=None, dlogits=None, ws=None, dev_status=None):
     """Loss of softmax(scale·logits) against a teacher's listed entries (ids [T, K] int32, −1 for
     an empty slot; logits [T, K] fp32, or log-probabilities with renormalize=False), and its
     gradient at the logits in grad_dtype (or the type of ``dlogits``).
@@ -782,12 +783,13 @@ def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weig
     _want(dev, ("teacher_ids", teacher_ids, (T, K), _I32T),
           ("teacher_logits", teacher_logits, (T, K), _F32), ("weight", weight, (T,), _F32),
           ("loss", loss, (T,), _F32), ("loss_sum", loss_sum, (1,), _F32), ("lse", lse, (T,), _F32),
-          ("dlogits", dlogits, (T, v), None), _status_spec(dev_status))
+          ("dlogits", dlogits, (T, v), None), _ws_spec(ws), _status_spec(dev_status))
+    ws, wsb = _workspace(ws, OP_DISTILL, T, K, v, N, dev)
     _check(_launch(lib().vp_distill, dev, _ptr(logits), _dt(logits), _ptr(teacher_ids),
                    _ptr(teacher_logits), _ptr(weight), T, v, K, N, 1 if renormalize else 0,
                    float(scale), float(grad_scale), _ptr(loss), _ptr(loss_sum), _ptr(lse),
-                   _ptr(dlogits), DTYPE_BF16 if dlogits is None else _dt(dlogits),
-                   _ptr(dev_status)), "vp_distill")
+                   _ptr(dlogits), DTYPE_BF16 if dlogits is None else _dt(dlogits), _ptr(ws),
+                   wsb, _ptr(dev_status)), "vp_distill")
     return {"loss": loss, "loss_sum": loss_sum, "lse": lse, "dlogits": dlogits}
 
 

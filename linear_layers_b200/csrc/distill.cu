@@ -7,10 +7,12 @@
 //   loss = w·(C − scale·A + P·log S)
 //   dlogits_j = grad_scale·w·scale·(P·exp(scale·(x_j − r))/S − Σ_{k: id_k = j} p_k)
 //
-// Every logit is needed twice, once for S and once for the gradient, and a
-// row of 50304 fp32 logits (201 KB) is wider than two SMs can buffer: so a
-// cluster of up to eight blocks holds one row, each block its slice in shared
-// memory.  HBM sees each logit read once and each gradient written once.
+// Every logit is needed twice, once for S and once for the gradient.  A
+// cluster of up to eight blocks holds one row, each block its slice in
+// registers (as the exponentials, so that each is taken once) while the next
+// rows' slices arrive in shared memory: HBM sees each logit read once and each
+// gradient written once, and the writes of one row run beside the reads of
+// the next.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -26,13 +28,13 @@
 namespace tpl {
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxSlices = 8;
-constexpr int kSeenWords = 1024;            // 32768 bits to notice a token listed twice
-constexpr int kChunkUnits = 2048;           // 32 KB of a slice, the grain of its refill
-constexpr int kMaxChunks = static_cast<int>((kDistillMaxSlice + 16 * kChunkUnits - 1) / (16 * kChunkUnits));
 
+// Blocks of NT streaming threads with R units each that the registers of an
+// SM are shared by.
+constexpr int blocks_per_sm(int R, int NT) {
+  return NT == 128 ? (R <= 4 ? 8 : 4) : NT == 256 || R <= 8 ? 2 : 1;
+}
 // 1-D bulk copy global -> this CTA's shared memory, completion counted in
 // bytes on `bar` (16-byte aligned addresses, size a multiple of 16).
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint32_t bytes,
@@ -44,9 +46,9 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
       : "memory");
 }
 
-// 4 bytes global -> shared, waited for by the same thread.
-__device__ __forceinline__ void copy_word(void* smem_dst, const void* gsrc) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gsrc)
+// 8 bytes global -> shared, waited for by the same thread.
+__device__ __forceinline__ void copy_entry(int2* smem_dst, const int2* gsrc) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem_dst)), "l"(gsrc)
                : "memory");
 }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -62,221 +64,335 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// A block's list of the listed tokens that lie in its slice, one for the row
-// at hand and one for the next: id −1 where an earlier entry names the same
-// token, p the token's summed probability.
-struct SlotLists {
-  int32_t* id[2];
-  float* p[2];
-  float* x;        // the tokens' logits, of the row at hand
-  int32_t* raw_id; // all slots of the next row
-  float* raw_t;
-  uint32_t* seen;  // [kSeenWords], zero between rows
+// ---------------------------------------------------------------------------
+// the teacher's slots
+// ---------------------------------------------------------------------------
+// What the rows' clusters need of the teacher, worked out once per row:
+// entries [T, K] of (token or −1, its probability), a token listed twice
+// merged into its first slot; info [T] of (P, C, any bad id, weight).
+struct Slots {
+  const int2* entries;
+  const float4* info;
+};
+
+constexpr int kPrepWarps = 4;
+constexpr int kSlots = kDistillMaxK / 32;   // slots per lane
+constexpr int kSeenWords = 1024;            // 32768 bits to notice a token listed twice
+
+// One warp per row.  The sums run over the lanes' slots and then by shuffles,
+// the same order every time.
+__global__ void __launch_bounds__(kPrepWarps * 32)
+    distill_slots_kernel(const DistillArgs a, int2* __restrict__ entries,
+                         float4* __restrict__ info) {
+  __shared__ uint32_t seen_bits[kPrepWarps][kSeenWords];
+  __shared__ int2 listed[kPrepWarps][kDistillMaxK];
+  grid_dependents_launch();   // the rows' kernel reads nothing of this one before it has ended
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepWarps + warp;
+  if (t >= a.T) return;
+  uint32_t* seen = seen_bits[warp];
+  for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
+  int32_t id[kSlots];
+  float lp[kSlots], p[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int s = lane + 32 * i;
+    id[i] = -1;
+    lp[i] = -CUDART_INF_F;
+    if (s < a.K) {
+      id[i] = a.ids[t * a.K + s];
+      lp[i] = a.teacher[t * a.K + s];
+    }
+  }
+  bool bad = false;
+  float top = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const bool out = id[i] < -1 || id[i] >= a.v;
+    bad |= out;
+    if (out || id[i] == -1) {   // the value of an empty slot is not looked at
+      id[i] = -1;
+      lp[i] = -CUDART_INF_F;
+    }
+    top = fmaxf(top, lp[i]);
+  }
+  if (a.renormalize) {
+    top = warp_max(top);
+    if (top == -CUDART_INF_F) top = 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      lp[i] -= top;
+      sum += expf(lp[i]);
+    }
+    sum = warp_sum(sum);
+    const float log_sum = sum == 0.0f ? 0.0f : logf(sum);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) lp[i] -= log_sum;
+  }
+  float P = 0.0f, C = 0.0f;
+  __syncwarp();
+  uint32_t again = 0;   // bit i: another slot had the bit of slot i's token
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    p[i] = id[i] == -1 ? 0.0f : expf(lp[i]);
+    P += p[i];
+    if (p[i] != 0.0f) C = fmaf(p[i], lp[i], C);
+    else id[i] = -1;
+    if (id[i] >= 0) {
+      const uint32_t bit = static_cast<uint32_t>(id[i]) & (kSeenWords * 32 - 1);
+      again |= ((atomicOr(&seen[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u) << i;
+    }
+  }
+  if (__any_sync(0xffffffffu, again)) {
+    // a token twice, or two tokens on one bit: looked up, slot group by slot group
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      listed[warp][lane + 32 * i] = make_int2(id[i], __float_as_int(p[i]));
+    __syncwarp();
+    bool twice = false;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (__any_sync(0xffffffffu, (again >> i) & 1u))
+        for (int q = 0; q < a.K; ++q)
+          twice |= id[i] >= 0 && listed[warp][q].x == id[i] && q != lane + 32 * i;
+    if (__any_sync(0xffffffffu, twice)) {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        if (32 * i >= a.K) break;
+        float sum = 0.0f;
+        bool first = true;
+        for (int q = 0; q < a.K; ++q) {   // in slot order
+          const int2 e = listed[warp][q];
+          if (e.x == id[i]) {
+            if (q < lane + 32 * i) first = false;
+            sum += __int_as_float(e.y);
+          }
+        }
+        p[i] = sum;
+        if (!first) id[i] = -1;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (lane + 32 * i < a.K)
+      entries[t * a.K + lane + 32 * i] = make_int2(id[i], __float_as_int(p[i]));
+  P = warp_sum(P);
+  C = warp_sum(C);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0)
+    info[t] = make_float4(P, C, bad ? 1.0f : 0.0f, a.weight ? a.weight[t] : 1.0f);
+}
+
+// ---------------------------------------------------------------------------
+// the rows
+// ---------------------------------------------------------------------------
+// One thread's R units between the two uses of a row.  fp32 logits are kept
+// as e = exp(scale·(x − m_w)) against the warp's maximum, one register each;
+// bf16 logits stay packed, two to a register, and their exponentials are taken
+// a second time: twice the rows fit the registers, and it is rows in flight
+// that hide the exchange between a row's blocks.
+template <typename IT, int R>
+struct Held;
+
+template <int R>
+struct Held<float, R> {
+  float e[R * 4];
+  float m;   // the warp's maximum, 0 for −inf
+  __device__ __forceinline__ void take(int i, uint4 w) { Unit<float>::unpack(w, e + 4 * i); }
+  __device__ __forceinline__ float maximum(float mx) const {
+#pragma unroll
+    for (int i = 0; i < R * 4; i += 2) mx = max3f(mx, e[i], e[i + 1]);
+    return mx;
+  }
+  __device__ __forceinline__ float sum(float ref, float sl) {
+    m = ref;
+    const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < R * 4; i += 2) {
+      const float2 y = __fmul2_rn(__fadd2_rn(make_float2(e[i], e[i + 1]), nr), sl2);
+      e[i] = ex2_approx(y.x);
+      e[i + 1] = ex2_approx(y.y);
+      s = __fadd2_rn(s, make_float2(e[i], e[i + 1]));
+    }
+    return s.x + s.y;
+  }
+  // coef·exp(scale·(x − ref)) of unit i
+  __device__ __forceinline__ void gradient(int i, float ref, float sl, float coef, float* g) const {
+    const float f = coef * ex2_approx((m - ref) * sl);
+    const float2 f2 = make_float2(f, f);
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      const float2 p = __fmul2_rn(make_float2(e[4 * i + q], e[4 * i + q + 1]), f2);
+      g[q] = p.x;
+      g[q + 1] = p.y;
+    }
+  }
+};
+
+template <int R>
+struct Held<__nv_bfloat16, R> {
+  uint4 w[R];
+  __device__ __forceinline__ void take(int i, uint4 x) { w[i] = x; }
+  __device__ __forceinline__ float maximum(float mx) const {
+    __nv_bfloat162 m2 = __float2bfloat162_rn(-CUDART_INF_F);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162*>(&q[j]));
+    }
+    return max3f(mx, __low2float(m2), __high2float(m2));
+  }
+  __device__ __forceinline__ float sum(float ref, float sl) {
+    const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float x[8];
+      Unit<__nv_bfloat16>::unpack(w[i], x);
+#pragma unroll
+      for (int q = 0; q < 8; q += 2) {
+        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[q], x[q + 1]), nr), sl2);
+        s = __fadd2_rn(s, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+      }
+    }
+    return s.x + s.y;
+  }
+  __device__ __forceinline__ void gradient(int i, float ref, float sl, float coef, float* g) const {
+    const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
+    const float2 c2 = make_float2(coef, coef);
+    uint4 q4 = w[i];   // unpacked anew, not kept in registers since the sum
+    asm volatile("" : "+r"(q4.x), "+r"(q4.y), "+r"(q4.z), "+r"(q4.w));
+    float x[8];
+    Unit<__nv_bfloat16>::unpack(q4, x);
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+      const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[q], x[q + 1]), nr), sl2);
+      const float2 p = __fmul2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), c2);
+      g[q] = p.x;
+      g[q + 1] = p.y;
+    }
+  }
 };
 
 // Persistent clusters of `slices` blocks; cluster c handles rows c, c + C, …
-// Block r of a cluster owns units [r·per, (r+1)·per) of each row, block 0 also
-// the row's edges.  The slice lies in shared memory in chunks; a chunk is
-// refilled with the next row's as soon as its gradient is written, so reads
-// of one row run beside the writes of the one before.  Of a block's warps the
-// last issues the copies, the one before looks after the teacher, the others
-// stream.  Per row:
-//   1. every streaming thread adds up its units as the chunks arrive;  barrier
-//   2. the teacher warp adds A and P of the block's own tokens and sends
-//      (r, S, A, P) to every block of the cluster, one 16-byte asynchronous
-//      store counted on the receiver's barrier; then it turns the next row's
-//      slots (loaded a row ahead) into probabilities;
+// Block r of a cluster owns units [r·per, (r+1)·per) of each row, per <= R·NT,
+// block 0 also the row's edges.  NT threads stream and one more warp looks
+// after the teacher.  Per row:
+//   1. the streaming threads take their R units from shared memory into
+//      registers and add them up; the teacher warp picks up the logits of the
+//      block's own listed tokens; barrier, and the buffer is refilled `nbuf`
+//      rows ahead;
+//   2. warp 0 sends the block's (r, S) to every block of the cluster, one
+//      16-byte asynchronous store counted on the receiver's barrier; the
+//      teacher warp sends A and P of its own tokens to block 0 the same way
+//      and lists its tokens of the next row;
 //   3. the blocks combine the records in slice order and the streaming
-//      threads write P·q over their slice, handing back chunk by chunk;
-//   4. the teacher warp, behind a barrier, writes the listed tokens over that.
-template <typename IT, typename GT>
-__global__ void __launch_bounds__(kMaxThreads + 64, 2)
-    distill_kernel(const DistillArgs a, int slices, int per, uint32_t buf_bytes, uint64_t wait_ns) {
+//      threads write P·q over their slice;
+//   4. the teacher warp, behind a barrier, writes the listed tokens over that;
+//      block 0's writes the loss.
+template <typename IT, typename GT, int R, int NT>
+__global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
+    distill_kernel(const DistillArgs a, const Slots slots, int slices, int per, int nbuf,
+                   uint32_t buf_stride, uint64_t wait_ns) {
   constexpr int kN = Unit<IT>::kN;
-  extern __shared__ __align__(128) uint8_t buffer[];      // the slice, then the slot lists
-  __shared__ __align__(16) float rec[2][kMaxSlices][4];   // [row parity][slice] (r, S, A, P)
+  constexpr int kWarps = NT / 32;
+  extern __shared__ __align__(128) uint8_t buffers[];       // the slices, then the slot lists
+  __shared__ __align__(16) float rec[2][kMaxSlices][4];     // [row parity][slice] (r, S)
+  __shared__ __align__(16) float own_rec[2][kMaxSlices][4]; // [row parity][slice] (A, P, r), block 0
   __shared__ __align__(8) uint64_t rec_bar[2];
-  __shared__ __align__(8) uint64_t full[kMaxChunks];      // a chunk of the row has landed
-  __shared__ __align__(8) uint64_t empty[kMaxChunks];     // ... and nothing reads it any more
-  __shared__ Sums wsum[2][kMaxWarps];
-  __shared__ float edge[2][2][8];          // [row parity] the row's two edges (block 0)
-  __shared__ float teacher_p[2], teacher_c[2];
-  __shared__ int teacher_bad[2];
+  __shared__ __align__(8) uint64_t own_bar[2];
+  __shared__ __align__(8) uint64_t load_bar[2];
+  __shared__ __align__(16) float wmax[2][kWarps], wsum[2][kWarps];   // [row parity] the warps' m, S
+  __shared__ float4 row_info[2];                            // [row parity]
 
   const int rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t cluster = blockIdx.x / static_cast<unsigned>(slices);
   const int64_t clusters = gridDim.x / static_cast<unsigned>(slices);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int threads = static_cast<int>(blockDim.x) - 64, warps = threads >> 5;
-  const int chunks = (per + kChunkUnits - 1) / kChunkUnits;
-  const float sl = a.scale * kLog2e, tau = 8.0f / sl;
+  const float sl = a.scale * kLog2e;
 
+  grid_dependents_launch();
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(&rec_bar[i], 1);
-    for (int c = 0; c < chunks; ++c) {
-      mbar_init(&full[c], 1);
-      // the streaming warps and, where a gradient may overwrite the logits, the teacher's
-      mbar_init(&empty[c], static_cast<uint32_t>(warps) + (a.dlogits != nullptr ? 1 : 0));
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&rec_bar[i], 1);
+      mbar_init(&own_bar[i], 1);
+      mbar_init(&load_bar[i], 1);
     }
     fence_mbarrier_init();
   }
   __syncthreads();
   if (slices > 1) cluster_sync_all();   // every barrier exists before a peer signals it
 
-  const volatile int never = 0;   // no role of the block cuts another's wait short
   auto timeout = [&]() {
     if (a.dev_status) atomicOr(a.dev_status, TP_DEVERR_TIMEOUT);
   };
-  // the row's softmax sums over all slices (every thread of a warp calls it)
+  auto wait_slice = [&](int k) {
+    if (!mbar_wait_cluster_bounded(&load_bar[nbuf == 2 ? k & 1 : 0],
+                                   static_cast<uint32_t>(nbuf == 2 ? k >> 1 : k) & 1u, wait_ns))
+      timeout();
+  };
+  // this block's sums of row k, and the row's over all slices (a whole warp
+  // calls it)
+  auto block_sums = [&](int k) {
+    if constexpr (kWarps == 4) {
+      const float4 m = *reinterpret_cast<const float4*>(wmax[k & 1]);
+      const float4 s = *reinterpret_cast<const float4*>(wsum[k & 1]);
+      const float mx = fmaxf(max3f(m.x, m.y, m.z), m.w);
+      const float r = mx == -CUDART_INF_F ? 0.0f : mx;
+      auto part = [&](float mi, float si) { return si * ex2_approx((mi - r) * sl); };
+      return Sums{mx, (part(m.x, s.x) + part(m.y, s.y)) + (part(m.z, s.z) + part(m.w, s.w)), 0.0f};
+    } else {
+      const int w = min(lane, kWarps - 1);
+      return join_sums(kWarps, Sums{wmax[k & 1][w], wsum[k & 1][w], 0.0f}, sl);
+    }
+  };
   auto row_sums = [&](int k) {
-    if (slices == 1) return join_sums(warps, wsum[k & 1][min(lane, warps - 1)], sl);
+    if (slices == 1) return block_sums(k);
     if (!mbar_wait_cluster_bounded(&rec_bar[k & 1], static_cast<uint32_t>(k >> 1) & 1u, wait_ns))
       timeout();
     const float* q = rec[k & 1][min(lane, slices - 1)];
     return join_sums(slices, Sums{q[0], q[1], 0.0f}, sl);
   };
 
-  if (warp == warps + 1) {
-    // ----------------------------------------------------------------- copies
-    if (lane == 0) {
-      int k = 0;
-      for (int64_t t = cluster; t < a.T; t += clusters, ++k) {
-        const RowShape<IT> shape(t * a.v, a.v);
-        const int u0 = min(rank * per, shape.units);
-        const int n = min(u0 + per, shape.units) - u0;
-        const char* src = static_cast<const char*>(a.logits) +
-                          (t * a.v + shape.head) * static_cast<int64_t>(sizeof(IT)) +
-                          static_cast<int64_t>(u0) * 16;
-        for (int c = 0; c < chunks; ++c) {
-          if (k > 0 && !mbar_wait_bounded(&empty[c], static_cast<uint32_t>(k - 1) & 1u, wait_ns, &never))
-            timeout();
-          const int units = min(max(n - c * kChunkUnits, 0), kChunkUnits);
-          mbar_arrive_expect_tx(&full[c], static_cast<uint32_t>(units) * 16u);
-          if (units > 0)
-            bulk_load(buffer + c * kChunkUnits * 16, src + static_cast<int64_t>(c) * kChunkUnits * 16,
-                      static_cast<uint32_t>(units) * 16u, &full[c]);
-        }
-      }
-    }
-  } else if (warp == warps) {
+  if (warp == kWarps) {
     // ---------------------------------------------------------------- teacher
-    SlotLists list;
-    {
-      uint8_t* at = buffer + buf_bytes;
-      const int bytes = a.K * 4;
-      for (int i = 0; i < 2; ++i) {
-        list.id[i] = reinterpret_cast<int32_t*>(at + 2 * i * bytes);
-        list.p[i] = reinterpret_cast<float*>(at + (2 * i + 1) * bytes);
-      }
-      list.raw_id = reinterpret_cast<int32_t*>(at + 4 * bytes);
-      list.raw_t = reinterpret_cast<float*>(at + 5 * bytes);
-      list.x = reinterpret_cast<float*>(at + 6 * bytes);
-      list.seen = reinterpret_cast<uint32_t*>(at + 7 * bytes);
-      for (int i = lane; i < kSeenWords; i += 32) list.seen[i] = 0;
-      __syncwarp();
-    }
-    // row t's slots on their way into the lists' raw places, lane by lane
+    int2* raw = reinterpret_cast<int2*>(buffers + nbuf * buf_stride);   // all of the next row's
+    int2* own_of[2] = {raw + a.K, raw + 2 * a.K};                      // the block's, by parity
+    float* own_x = reinterpret_cast<float*>(raw + 3 * a.K);            // their logits
+    float4 next_info = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto fetch = [&](int64_t t) {
-      for (int s = lane; s < a.K; s += 32) {
-        copy_word(&list.raw_id[s], a.ids + t * a.K + s);
-        copy_word(&list.raw_t[s], a.teacher + t * a.K + s);
-      }
+#pragma unroll 4
+      for (int s = lane; s < a.K; s += 32) copy_entry(&raw[s], &slots.entries[t * a.K + s]);
+      next_info = slots.info[t];
     };
-    // probabilities of row t's slots and the list of this block's own; how many
+    // the block's own tokens of row t, in slot order; how many
     auto prepare = [&](int64_t t, int b) -> int {
       const RowShape<IT> shape(t * a.v, a.v);
       const int own0 = shape.head + min(rank * per, shape.units) * kN;
       const int own1 = shape.head + min(rank * per + per, shape.units) * kN;
       const int body1 = shape.head + shape.units * kN;
+      if (lane == 0) row_info[b] = next_info;
       copy_wait();
-      bool bad = false;
-      float top = -CUDART_INF_F;
-      for (int s = lane; s < a.K; s += 32) {
-        const int id = list.raw_id[s];
-        const bool out = id < -1 || id >= a.v;
-        bad |= out;
-        if (out || id == -1) {   // the value of an empty slot is not looked at
-          list.raw_id[s] = -1;
-          list.raw_t[s] = -CUDART_INF_F;
-        }
-        top = fmaxf(top, list.raw_t[s]);
-      }
-      float log_sum = 0.0f;
-      if (a.renormalize) {
-        top = warp_max(top);
-        if (top == -CUDART_INF_F) top = 0.0f;
-        float sum = 0.0f;
-        for (int s = lane; s < a.K; s += 32) sum += expf(list.raw_t[s] - top);
-        sum = warp_sum(sum);
-        log_sum = sum == 0.0f ? 0.0f : logf(sum);
-      } else {
-        top = 0.0f;
-      }
-      float P = 0.0f, C = 0.0f;
       int n = 0;
+#pragma unroll 4
       for (int s0 = 0; s0 < a.K; s0 += 32) {
-        int id = -1;
-        float lp = 0.0f, p = 0.0f;
-        if (s0 + lane < a.K) {
-          id = list.raw_id[s0 + lane];
-          lp = (list.raw_t[s0 + lane] - top) - log_sum;
-          if (id != -1) p = expf(lp);
-        }
-        P += p;
-        if (p != 0.0f) C = fmaf(p, lp, C);
-        const bool own = p != 0.0f && ((id >= own0 && id < own1) ||
-                                       (rank == 0 && (id < shape.head || id >= body1)));
+        int2 e = make_int2(-1, 0);
+        if (s0 + lane < a.K) e = raw[s0 + lane];
+        const bool own = (e.x >= own0 && e.x < own1) ||
+                         (rank == 0 && e.x >= 0 && (e.x < shape.head || e.x >= body1));
         const uint32_t mask = __ballot_sync(0xffffffffu, own);
-        if (own) {
-          const int at = n + __popc(mask & ((1u << lane) - 1u));
-          list.id[b][at] = id;
-          list.p[b][at] = p;
-        }
+        if (own) own_of[b][n + __popc(mask & ((1u << lane) - 1u))] = e;
         n += __popc(mask);
-      }
-      P = warp_sum(P);
-      C = warp_sum(C);
-      bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) {
-        teacher_p[b] = P;
-        teacher_c[b] = C;
-        teacher_bad[b] = bad;
-      }
-      __syncwarp();
-      // A token listed twice shows as a bit of `seen` that was set already;
-      // that it is one, and not two tokens on one bit, is looked up.
-      bool twice = false;
-      for (int e = lane; e < n; e += 32) {
-        const uint32_t bit = static_cast<uint32_t>(list.id[b][e]) & (kSeenWords * 32 - 1);
-        if ((atomicOr(&list.seen[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u)
-          for (int q = 0; q < n; ++q) twice |= q != e && list.id[b][q] == list.id[b][e];
-      }
-      __syncwarp();
-      for (int e = lane; e < n; e += 32)
-        list.seen[(static_cast<uint32_t>(list.id[b][e]) & (kSeenWords * 32 - 1)) >> 5] = 0;
-      if (__any_sync(0xffffffffu, twice)) {   // one entry per token, summed in slot order
-        for (int e = lane; e < n; e += 32) {
-          const int id = list.id[b][e];
-          float sum = 0.0f;
-          bool first = true;
-          for (int q = 0; q < n; ++q)
-            if (list.id[b][q] == id) {
-              if (q < e) first = false;
-              sum += list.p[b][q];
-            }
-          list.raw_id[e] = first ? id : -1;
-          list.raw_t[e] = sum;
-        }
-        __syncwarp();
-        for (int e = lane; e < n; e += 32) {
-          list.id[b][e] = list.raw_id[e];
-          list.p[b][e] = list.raw_t[e];
-        }
       }
       __syncwarp();
       return n;
     };
 
+    grid_dependency_wait();   // the entries are there
     int n = 0;
     if (cluster < a.T) {
       fetch(cluster);
@@ -289,35 +405,34 @@ __global__ void __launch_bounds__(kMaxThreads + 64, 2)
       const RowShape<IT> shape(t * a.v, a.v);
       const int own0 = shape.head + min(rank * per, shape.units) * kN;
       const int own1 = shape.head + min(rank * per + per, shape.units) * kN;
-      const IT* slice = reinterpret_cast<const IT*>(buffer);
-      auto value = [&](int j) {
-        if (a.dlogits == nullptr) return to_f32(static_cast<const IT*>(a.logits)[t * a.v + j]);
-        if (j >= own0 && j < own1) return to_f32(slice[j - own0]);
-        return j < shape.head ? edge[par][0][j] : edge[par][1][j - shape.head - shape.units * kN];
-      };
-      const float w = a.weight ? a.weight[t] : 1.0f;
-      named_barrier_sync(1, static_cast<uint32_t>(threads) + 32);   // the block's sums and edges
-      if (a.dlogits != nullptr)
-        for (int c = 0; c < chunks; ++c)   // landed: the streaming warps have waited for them
-          if (!mbar_wait_bounded(&full[c], static_cast<uint32_t>(k) & 1u, wait_ns, &never)) timeout();
-      const Sums own = join_sums(warps, wsum[par][min(lane, warps - 1)], sl);
-      const float own_ref = own.m == -CUDART_INF_F ? 0.0f : own.m;
-      float A = 0.0f, Pown = 0.0f;
+      const int2* own = own_of[par];
+      const IT* slice =
+          reinterpret_cast<const IT*>(buffers + (nbuf == 2 ? par : 0) * buf_stride);
+      if (rank == 0 && lane == 0 && slices > 1)
+        mbar_arrive_expect_tx(&own_bar[par], static_cast<uint32_t>(slices) * 16u);
+      wait_slice(k);
+#pragma unroll 4
       for (int e = lane; e < n; e += 32) {
-        const int id = list.id[par][e];
-        if (id >= 0) {
-          const float x = value(id);
-          list.x[e] = x;
-          A = fmaf(list.p[par][e], x - own_ref, A);
-          Pown += list.p[par][e];
-        }
+        const int id = own[e].x;
+        own_x[e] = id >= own0 && id < own1
+                       ? to_f32(slice[id - own0])
+                       : to_f32(static_cast<const IT*>(a.logits)[t * a.v + id]);
+      }
+      named_barrier_sync(1, NT + 32);   // the slice has been read, the warps' sums are there
+      const float block_m = block_sums(k).m;
+      const float block_ref = block_m == -CUDART_INF_F ? 0.0f : block_m;
+      float A = 0.0f, P_own = 0.0f;
+#pragma unroll 4
+      for (int e = lane; e < n; e += 32) {
+        const float p = __int_as_float(own[e].y);
+        A = fmaf(p, own_x[e] - block_ref, A);
+        P_own += p;
       }
       A = warp_sum(A);
-      Pown = warp_sum(Pown);
-      if (slices > 1 && lane < slices)
-        st_async_v4(mapa_shared(&rec[par][rank][0], static_cast<uint32_t>(lane)),
-                    mapa_shared(&rec_bar[par], static_cast<uint32_t>(lane)), own.m, own.s, A, Pown);
-      if (a.dlogits != nullptr && lane < chunks) mbar_arrive(&empty[lane]);   // behind the shuffles: every lane has read
+      P_own = warp_sum(P_own);
+      if (slices > 1 && lane == 0)
+        st_async_v4(mapa_shared(&own_rec[par][rank][0], 0), mapa_shared(&own_bar[par], 0), A, P_own,
+                    block_ref, 0.0f);
       int n_next = 0;
       if (t + clusters < a.T) {
         n_next = prepare(t + clusters, par ^ 1);
@@ -325,207 +440,207 @@ __global__ void __launch_bounds__(kMaxThreads + 64, 2)
       }
       const Sums all = row_sums(k);
       const float ref = all.m == -CUDART_INF_F ? 0.0f : all.m;
-      const float P = teacher_p[par];
-      const bool any_bad = teacher_bad[par] != 0;
+      const float4 info = row_info[par];
+      const float P = info.x, w = info.w;
+      const bool any_bad = info.z != 0.0f;
       const bool dead = w == 0.0f || (P == 0.0f && !any_bad);
       if (rank == 0) {
         if (slices > 1) {   // the slices' A moved to the common reference, in slice order
+          if (!mbar_wait_cluster_bounded(&own_bar[par], static_cast<uint32_t>(k >> 1) & 1u, wait_ns))
+            timeout();
           A = 0.0f;
           for (int i = 0; i < slices; ++i) {
-            const float* q = rec[par][i];
-            if (q[3] != 0.0f) A += fmaf((q[0] == -CUDART_INF_F ? 0.0f : q[0]) - ref, q[3], q[2]);
+            const float* q = own_rec[par][i];
+            if (q[1] != 0.0f) A += fmaf(q[2] - ref, q[1], q[0]);
           }
         }
         if (lane == 0) {
           const float log_s = logf(all.s);
-          const float loss = fmaf(P, log_s, fmaf(-a.scale, A, teacher_c[par]));
+          const float loss = fmaf(P, log_s, fmaf(-a.scale, A, info.y));
           a.loss[t] = dead ? 0.0f : any_bad ? CUDART_NAN_F : w * loss;
           if (a.lse) a.lse[t] = fmaf(a.scale, ref, log_s);
           if (!dead && any_bad && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
         }
       }
       if (a.dlogits != nullptr) {
-        named_barrier_sync(2, static_cast<uint32_t>(threads) + 32);   // P·q is written
+        named_barrier_sync(2, NT + 32);   // P·q is written
         if (!dead) {
           const float c = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale;
           const float inv = 1.0f / all.s;
           GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
-          for (int e = lane; e < n; e += 32) {
-            const int id = list.id[par][e];
-            if (id >= 0)
-              put(out + id, c * (P * (ex2_approx((list.x[e] - ref) * sl) * inv) - list.p[par][e]));
-          }
+#pragma unroll 4
+          for (int e = lane; e < n; e += 32)
+            put(out + own[e].x, c * (P * (ex2_approx((own_x[e] - ref) * sl) * inv) -
+                                     __int_as_float(own[e].y)));
         }
       }
       n = n_next;
     }
   } else {
     // -------------------------------------------------------------- streaming
-    const uint4* slice = reinterpret_cast<const uint4*>(buffer);
-    auto release = [&](int c) {   // this warp has read chunk c for the last time
-      __syncwarp();
-      if (lane == 0) {
-        fence_proxy_async_smem();   // the reads come before the refill's writes
-        mbar_arrive(&empty[c]);
-      }
+    auto issue = [&](int b, int64_t t) {   // one thread: this block's slice of row t
+      const RowShape<IT> shape(t * a.v, a.v);
+      const int u0 = min(rank * per, shape.units), u1 = min(u0 + per, shape.units);
+      const uint32_t bytes = static_cast<uint32_t>(u1 - u0) * 16u;
+      mbar_arrive_expect_tx(&load_bar[b], bytes);
+      const char* src = static_cast<const char*>(a.logits) +
+                        (t * a.v + shape.head) * static_cast<int64_t>(sizeof(IT)) +
+                        static_cast<int64_t>(u0) * 16;
+      uint8_t* dst = buffers + b * buf_stride;
+      for (uint32_t off = 0; off < bytes; off += 16384u)
+        bulk_load(dst + off, src + off, min(bytes - off, 16384u), &load_bar[b]);
     };
-    constexpr int kBatch = 16 / kN;   // units a thread has in hand: 16 logits
+    if (tid == 32)
+      for (int b = 0; b < nbuf; ++b)
+        if (cluster + b * clusters < a.T) issue(b, cluster + b * clusters);
     constexpr uint32_t kInf = Unit<IT>::kMinusInf;
     const uint4 fill = make_uint4(kInf, kInf, kInf, kInf);
+    // the row's edges: thread i of block 0 the i-th element of the head, thread
+    // 32 + i of the tail; loaded a row ahead
+    auto edge_of = [&](const RowShape<IT>& shape) {
+      if (rank == 0 && tid < shape.head) return tid;
+      if (rank == 0 && tid >= 32 && tid < 32 + shape.tail)
+        return shape.head + shape.units * kN + tid - 32;
+      return -1;
+    };
+    auto load_edge = [&](int64_t t) {
+      const int j = t < a.T ? edge_of(RowShape<IT>(t * a.v, a.v)) : -1;
+      return j >= 0 ? to_f32(static_cast<const IT*>(a.logits)[t * a.v + j]) : -CUDART_INF_F;
+    };
+    float next_edge = load_edge(cluster);
     int k = 0;
     for (int64_t t = cluster; t < a.T; t += clusters, ++k) {
       const int par = k & 1;
       const RowShape<IT> shape(t * a.v, a.v);
       const int u0 = min(rank * per, shape.units);
       const int n = min(u0 + per, shape.units) - u0;
-      const float w = a.weight ? a.weight[t] : 1.0f;
+      const uint4* slice =
+          reinterpret_cast<const uint4*>(buffers + (nbuf == 2 ? par : 0) * buf_stride);
       // this row's records: one arrival here, 16 bytes from each slice
       if (tid == 0 && slices > 1)
         mbar_arrive_expect_tx(&rec_bar[par], static_cast<uint32_t>(slices) * 16u);
-      const bool is_head = rank == 0 && tid < shape.head;
-      const bool is_tail = rank == 0 && tid >= 32 && tid < 32 + shape.tail;
-      const int64_t edge_j =
-          is_head ? tid : shape.head + static_cast<int64_t>(shape.units) * kN + tid - 32;
-      float edge_x = 0.0f;
-      if (is_head || is_tail) {
-        edge_x = to_f32(static_cast<const IT*>(a.logits)[t * a.v + edge_j]);
-        edge[par][is_head ? 0 : 1][is_head ? tid : tid - 32] = edge_x;
-      }
-      RowSums sums;
-      for (int c = 0; c < chunks; ++c) {
-        if (!mbar_wait_bounded(&full[c], static_cast<uint32_t>(k) & 1u, wait_ns, &never)) timeout();
-        const int end = min((c + 1) * kChunkUnits, n);
-        for (int u = c * kChunkUnits + tid; u < end; u += kBatch * threads) {
-          float x[kBatch * kN];
+      const int my_edge = edge_of(shape);
+      const float edge_x = next_edge;
+      wait_slice(k);
+      Held<IT, R> held;
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            Unit<IT>::unpack(u + i * threads < end ? slice[u + i * threads] : fill, x + i * kN);
-          sums.add<kBatch * kN, false>(x, sl, tau);
-        }
-        if (a.dlogits == nullptr) release(c);
+      for (int i = 0; i < R; ++i) {
+        const int u = tid + i * NT;
+        held.take(i, u < n ? slice[u] : fill);
       }
-      if (is_head || is_tail) sums.add1<false>(edge_x, sl, tau);
-      const Sums ws = warp_sums(sums, sl);
-      if (lane == 0) wsum[par][warp] = ws;
-      named_barrier_sync(1, static_cast<uint32_t>(threads) + 32);
-      if (a.dlogits == nullptr) {
-        if (slices > 1) row_sums(k);   // the records of row k+2 reuse this row's places
-        continue;
+      const float m_w = warp_max(held.maximum(edge_x));
+      const float ref_w = m_w == -CUDART_INF_F ? 0.0f : m_w;
+      float s_w = held.sum(ref_w, sl);
+      if (my_edge >= 0) s_w += ex2_approx((edge_x - ref_w) * sl);
+      s_w = warp_sum(s_w);
+      if (lane == 0) {
+        wmax[par][warp] = m_w;
+        wsum[par][warp] = s_w;
+      }
+      named_barrier_sync(1, NT + 32);
+      if (tid == 32 && t + nbuf * clusters < a.T) {
+        fence_proxy_async_smem();
+        issue(nbuf == 2 ? par : 0, t + nbuf * clusters);
+      }
+      next_edge = load_edge(t + clusters);
+      if (slices > 1 && warp == 0) {
+        const Sums own = block_sums(k);
+        if (lane < slices)
+          st_async_v4(mapa_shared(&rec[par][rank][0], static_cast<uint32_t>(lane)),
+                      mapa_shared(&rec_bar[par], static_cast<uint32_t>(lane)), own.m, own.s, 0.0f,
+                      0.0f);
       }
       const Sums all = row_sums(k);
+      if (a.dlogits == nullptr) continue;
       const float ref = all.m == -CUDART_INF_F ? 0.0f : all.m;
-      const float P = teacher_p[par];
-      const bool any_bad = teacher_bad[par] != 0;
+      const float4 info = row_info[par];
+      const float P = info.x, w = info.w;
+      const bool any_bad = info.z != 0.0f;
       const bool dead = w == 0.0f || (P == 0.0f && !any_bad);
       const float coef = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale * (P * (1.0f / all.s));
       GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
       GT* dst = out + shape.head + static_cast<int64_t>(u0) * kN;
-      const float2 nr = make_float2(-ref, -ref), sl2 = make_float2(sl, sl);
-      const float2 c2 = make_float2(coef, coef);
-      for (int c = 0; c < chunks; ++c) {
-        const int end = min((c + 1) * kChunkUnits, n);
-        if (dead) {
-          const float z[kN] = {};
-          for (int u = c * kChunkUnits + tid; u < end; u += threads)
-            put_unit<kN>(dst + static_cast<int64_t>(u) * kN, z);
-        } else {
-          for (int u = c * kChunkUnits + tid; u < end; u += kBatch * threads) {
-            uint4 w4[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              w4[i] = u + i * threads < end ? slice[u + i * threads] : fill;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              float x[kN];
-              Unit<IT>::unpack(w4[i], x);
-#pragma unroll
-              for (int q = 0; q < kN; q += 2) {
-                const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[q], x[q + 1]), nr), sl2);
-                const float2 g = __fmul2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), c2);
-                x[q] = g.x;
-                x[q + 1] = g.y;
-              }
-              if (u + i * threads < end)
-                put_unit<kN>(dst + static_cast<int64_t>(u + i * threads) * kN, x);
-            }
-          }
+      for (int i = 0; i < R; ++i) {
+        const int u = tid + i * NT;
+        if (u < n) {
+          float g[kN] = {};
+          if (!dead) held.gradient(i, ref, sl, coef, g);
+          put_unit<kN>(dst + static_cast<int64_t>(u) * kN, g);
         }
-        release(c);
       }
-      if (is_head || is_tail)
-        put(out + edge_j, dead ? 0.0f : coef * ex2_approx((edge_x - ref) * sl));
+      if (my_edge >= 0)
+        put(out + my_edge, dead ? 0.0f : coef * ex2_approx((edge_x - ref) * sl));
       // the teacher warp's writes come after these; nothing here waits
-      named_barrier_arrive(2, static_cast<uint32_t>(threads) + 32);
+      named_barrier_arrive(2, NT + 32);
     }
   }
   __syncthreads();
   if (slices > 1) cluster_sync_all();   // every peer's record into this block has landed
 }
 
-template <typename IT, typename GT>
-tp_status distill_launch_t(const DistillArgs& a, cudaStream_t stream) {
-  constexpr int64_t kN = Unit<IT>::kN;
-  const int64_t units = (a.v + kN - 1) / kN;
-  // Slices of a row: at most 108 KB, so that two blocks share an SM and one's
-  // barriers and exchanges run beside the other's sweeps; with few rows, more
-  // of them while each keeps 4 KB.
-  int slices = 1;
-  while (slices < kMaxSlices &&
-         (units * 16 > 108 * 1024 * slices ||
-          (a.T * slices * 2 <= num_sms() && units * 16 >= 8192 * slices)))
-    slices *= 2;
-  if (const char* e = getenv("TPX_SL")) slices = atoi(e);
-  const int per = static_cast<int>((units + slices - 1) / slices);
-  const int64_t slice = (static_cast<int64_t>(per) * 16 + 127) & ~int64_t{127};
-  if (slice > kDistillMaxSlice) return TP_ERR_UNSUPPORTED;
-  int threads = slice <= 16 * 1024 ? 128 : slice <= 50 * 1024 ? 256 : 512;
-  if (const char* e = getenv("TPX_NT")) threads = atoi(e);
-  const int smem = static_cast<int>(slice + 28 * a.K + 4 * kSeenWords);   // and the slot lists
+// One launch: rows in slices of `per` units.
+template <typename IT, typename GT, int R, int NT>
+tp_status launch(const DistillArgs& a, const Slots& slots, int slices, int per,
+                 cudaStream_t stream) {
+  // two buffers (rows ahead) while the blocks that the registers allow still
+  // fit an SM, else one
+  constexpr int kBlocks = blocks_per_sm(R, NT);
+  constexpr int64_t kSmem = 224 * 1024 / kBlocks - 2048;   // a block's share, less its static part
+  const int64_t stride = (static_cast<int64_t>(per) * 16 + 127) & ~int64_t{127};
+  const int64_t lists = 28 * a.K;
+  const int nbuf = 2 * stride + lists <= kSmem ? 2 : 1;
+  const int smem = static_cast<int>(nbuf * stride + lists);
+  auto kernel = distill_kernel<IT, GT, R, NT>;
   int dev = 0;
   cudaGetDevice(&dev);
   static bool configured[64] = {false};
   if (!configured[dev & 63]) {
-    if (cudaFuncSetAttribute(distill_kernel<IT, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kDistillMaxSlice + 28 * kDistillMaxK +
-                                              4 * kSeenWords)) != cudaSuccess ||
-        cudaFuncSetAttribute(distill_kernel<IT, GT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    constexpr int64_t kMost = ((R * NT * 16 + 127) & ~127) + 28 * kDistillMaxK;
+    static_assert(kMost <= 224 * 1024, "shared memory of one block");
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kMost > kSmem ? kMost : kSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return TP_ERR_CUDA;
     configured[dev & 63] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(static_cast<unsigned>(threads + 64));
+  cfg.blockDim = dim3(NT + 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(slices);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // programmatic dependent launch: the blocks set up and read their first
+  // rows while the slots' kernel runs; only the teacher warps wait for it
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   // clusters that can be resident at once, by launch shape
-  struct Shape {
-    int dev = -1, slices = 0, smem = 0, threads = 0, clusters = 0;
+  struct Resident {
+    int dev = -1, slices = 0, smem = 0, clusters = 0;
   };
-  static thread_local Shape last;
-  if (last.dev != dev || last.slices != slices || last.smem != smem || last.threads != threads) {
+  static thread_local Resident last;
+  if (last.dev != dev || last.slices != slices || last.smem != smem) {
     int n = 0;
     cfg.gridDim = dim3(static_cast<unsigned>(slices * num_sms()));
-    if (cudaOccupancyMaxActiveClusters(&n, distill_kernel<IT, GT>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
       n = num_sms() / slices;
     }
     last.dev = dev;
     last.slices = slices;
     last.smem = smem;
-    last.threads = threads;
     last.clusters = n;
   }
   const int64_t clusters = a.T < last.clusters ? a.T : last.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * slices));
-  if (cudaLaunchKernelEx(&cfg, distill_kernel<IT, GT>, a, slices, per,
-                         static_cast<uint32_t>(slice), wait_limit_ns()) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, a, slots, slices, per, nbuf, static_cast<uint32_t>(stride),
+                         wait_limit_ns()) != cudaSuccess) {
     cudaGetLastError();
     return TP_ERR_CUDA;
   }
@@ -533,19 +648,59 @@ tp_status distill_launch_t(const DistillArgs& a, cudaStream_t stream) {
   return TP_OK;
 }
 
+template <typename IT, typename GT>
+tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_t stream) {
+  constexpr int kN = Unit<IT>::kN;
+  const int64_t units = (a.v + kN - 1) / kN;
+  // Slices of a row: as few as hold it.  A row of 50304 fp32 logits in
+  // gradient steps of 8192 rows took 411 us on two blocks of 512 threads, 643 us
+  // on eight of 128: every exchange waits for the last of the row's blocks.
+  // With few rows, more slices while each keeps 4 KB.
+  int slices = 1;
+  while (slices < kMaxSlices &&
+         (units > 22 * 480 * slices ||
+          (a.T * slices * 2 <= num_sms() && units * 16 >= 8192 * slices)))
+    slices *= 2;
+  if (const char* e = getenv("TPX_SL")) slices = atoi(e);
+  const int per = static_cast<int>((units + slices - 1) / slices);
+  if (per <= 4 * 128) return launch<IT, GT, 4, 128>(a, slots, slices, per, stream);
+  if (per <= 8 * 128) return launch<IT, GT, 8, 128>(a, slots, slices, per, stream);
+  if (per <= 13 * 128) return launch<IT, GT, 13, 128>(a, slots, slices, per, stream);
+  if (per <= 10 * 256) return launch<IT, GT, 10, 256>(a, slots, slices, per, stream);
+  if (per <= 13 * 256) return launch<IT, GT, 13, 256>(a, slots, slices, per, stream);
+  if (per <= 8 * 512) return launch<IT, GT, 8, 512>(a, slots, slices, per, stream);
+  if (per <= 10 * 512) return launch<IT, GT, 10, 512>(a, slots, slices, per, stream);
+  if (per <= 13 * 512) return launch<IT, GT, 13, 512>(a, slots, slices, per, stream);
+  if (per <= 16 * 512) return launch<IT, GT, 16, 512>(a, slots, slices, per, stream);
+  if (per <= 22 * 480) return launch<IT, GT, 22, 480>(a, slots, slices, per, stream);
+  return TP_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
+size_t distill_ws_bytes(int64_t T, int64_t K) {
+  return static_cast<size_t>(T) * (sizeof(float4) + K * sizeof(int2));
+}
+
 tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, float* loss_sum,
-                         cudaStream_t stream) {
+                         void* ws, cudaStream_t stream) {
+  float4* info = static_cast<float4*>(ws);
+  int2* entries = reinterpret_cast<int2*>(info + a.T);
+  distill_slots_kernel<<<static_cast<unsigned>((a.T + kPrepWarps - 1) / kPrepWarps),
+                         kPrepWarps * 32, 0, stream>>>(a, entries, info);
+  note_launches(1);
+  if (cudaGetLastError() != cudaSuccess) return TP_ERR_CUDA;
+  const Slots slots{entries, info};
+  const bool f32_grad = a.dlogits && grad_dt == TP_DTYPE_F32;
   tp_status st;
   if (dt == TP_DTYPE_BF16)
-    st = a.dlogits && grad_dt == TP_DTYPE_F32 ? distill_launch_t<__nv_bfloat16, float>(a, stream)
-                                              : distill_launch_t<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    st = f32_grad ? distill_launch_t<__nv_bfloat16, float>(a, slots, stream)
+                  : distill_launch_t<__nv_bfloat16, __nv_bfloat16>(a, slots, stream);
   else
-    st = a.dlogits && grad_dt == TP_DTYPE_F32 ? distill_launch_t<float, float>(a, stream)
-                                              : distill_launch_t<float, __nv_bfloat16>(a, stream);
+    st = f32_grad ? distill_launch_t<float, float>(a, slots, stream)
+                  : distill_launch_t<float, __nv_bfloat16>(a, slots, stream);
   if (st) return st;
-  return loss_sum ? loss_sum_launch(a.loss, a.T, loss_sum, stream) : TP_OK;
+  return loss_sum ? loss_sum_launch(a.loss, a.T, loss_sum, stream, true) : TP_OK;
 }
 
 }  // namespace tpl

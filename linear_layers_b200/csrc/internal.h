@@ -133,8 +133,10 @@ tp_status sp_ln_bwd_launch(const void* dy, const void* dhs_in, const void* hs, c
                            uint64_t seed, uint64_t offset, void* dx, void* dres, float* dgamma,
                            float* dbeta, float* dbias, void* ws, cudaStream_t stream);
 
-// loss_sum = Σ_t loss[t] in a fixed order (vocab.cu).
-tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStream_t stream);
+// loss_sum = Σ_t loss[t] in a fixed order (vocab.cu).  `early`: set up while
+// the kernel before it on the stream still runs (it waits for that one's end).
+tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStream_t stream,
+                          bool early = false);
 
 // Log-probabilities, entropy and top alternatives, and their gradient
 // (logprobs.cu): see vp_logprobs_fwd / vp_logprobs_bwd.
@@ -175,9 +177,8 @@ tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_
 
 // Distillation from a teacher's top entries: see vp_distill.
 constexpr int kDistillMaxK = 256;
-// Bytes of a block's slices of logits in shared memory; eight blocks hold a
-// row, so a row may have 8·217088 bytes.
-constexpr int64_t kDistillMaxSlice = 212 * 1024;
+// The widest row: eight blocks of 480 threads hold 88 logits a thread.
+constexpr int64_t kDistillMaxV = 8 * 480 * 88;
 struct DistillArgs {
   const void* logits;
   const int32_t* ids;       // [T, K], -1: empty slot
@@ -191,8 +192,9 @@ struct DistillArgs {
   void* dlogits;            // nullable
   int32_t* dev_status;
 };
+size_t distill_ws_bytes(int64_t T, int64_t K);
 tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, float* loss_sum,
-                         cudaStream_t stream);
+                         void* ws, cudaStream_t stream);
 
 // Counts every kernel the library enqueues (tp_launch_count).
 void note_launches(int n);

@@ -120,6 +120,12 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Let the grid that depends on this one be set up now; its own
+// grid_dependency_wait still waits for all of this grid's work.
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tensor copies through a CUtensorMap in kernel parameter space)
 // ---------------------------------------------------------------------------

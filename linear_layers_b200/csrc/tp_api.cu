@@ -296,6 +296,8 @@ size_t tp_workspace_bytes(tp_op op, int64_t M, int64_t h, int64_t F, int32_t N) 
       return linear_xent_ws_bytes(M, F);
     case TP_OP_LINEAR_LOGPROBS:   // (T, h, v, N): slice statistics + target logits
       return linear_logprobs_ws_bytes(M, F);
+    case TP_OP_DISTILL:       // (T, K, v, N): the teacher's entries and per-row numbers
+      return align256(distill_ws_bytes(M, h));
     case TP_OP_SP_LN_BWD:     // (M, h, h, N): per-block partial parameter gradients
       return sp_ln_bwd_ws_bytes(M, h);
     case TP_OP_ATTENTION_BWD: // (b·s, n_heads, 64, N): rowsum(dO ⊙ O), fp32 dQ accumulator
@@ -852,19 +854,20 @@ tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids
                      const float* teacher_logits, const float* weight, int64_t T, int64_t v,
                      int32_t K, int32_t N, int32_t renormalize, float scale, float grad_scale,
                      float* loss, float* loss_sum, float* lse, void* dlogits, tp_dtype grad_dt,
-                     int32_t* dev_status, void* stream) {
+                     void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
   if (!logits || !teacher_ids || !teacher_logits || !loss) return TP_ERR_NULL;
   if (!dtype_ok(dt) || (dlogits && !dtype_ok(grad_dt))) return TP_ERR_DTYPE;
   if (!dims_ok({T, v, K}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
-  if (K > kDistillMaxK || v * elem_bytes(dt) > 8 * kDistillMaxSlice) return TP_ERR_UNSUPPORTED;
-  if (!ptrs_aligned({logits, dlogits}) ||
+  if (K > kDistillMaxK || v > kDistillMaxV) return TP_ERR_UNSUPPORTED;
+  if (!ptrs_aligned({logits, dlogits, ws}) ||
       !words_aligned({teacher_ids, teacher_logits, weight, loss, loss_sum, lse}, 4))
     return TP_ERR_ALIGN;
   if (logits == dlogits && dt != grad_dt) return TP_ERR_UNSUPPORTED;
+  if (ws == nullptr || ws_bytes < distill_ws_bytes(T, K)) return TP_ERR_WORKSPACE;
   if (tp_status s = require_sm100()) return s;
   DistillArgs a{logits, teacher_ids, teacher_logits, weight, T,   v,       K, renormalize != 0,
                 scale,  grad_scale,  loss,           lse,    dlogits, dev_status};
-  return distill_launch(a, dt, grad_dt, loss_sum, as_stream(stream));
+  return distill_launch(a, dt, grad_dt, loss_sum, ws, as_stream(stream));
 }
 
 tp_status tp_linear_logprobs_fwd(const void* H, const void* E, const int64_t* targets, int64_t T,

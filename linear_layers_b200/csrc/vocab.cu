@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(kXentThreads)
 // loss_sum = Σ_t loss[t], one block, fixed order (deterministic).
 __global__ void __launch_bounds__(1024) loss_sum_kernel(const float* loss, int64_t T, float* out) {
   __shared__ float part[1024];
+  grid_dependency_wait();   // the losses are there
   float s = 0.f;
   for (int64_t i = threadIdx.x; i < T; i += 1024) s += loss[i];
   part[threadIdx.x] = s;
@@ -526,10 +527,21 @@ __global__ void __launch_bounds__(kCombWarps * 32) linear_xent_combine_kernel(
 
 }  // namespace
 
-tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStream_t stream) {
-  loss_sum_kernel<<<1, 1024, 0, stream>>>(loss, T, loss_sum);
+tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStream_t stream,
+                          bool early) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, loss_sum_kernel, loss, T, loss_sum) != cudaSuccess)
+    return TP_ERR_CUDA;
   note_launches(1);
-  return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+  return TP_OK;
 }
 
 namespace {

@@ -133,15 +133,17 @@ def test_logprobs_abi(L):
 
 def test_distill_abi(L):
     f = lambda **k: call(L.vp_distill,  # noqa: E731
-                         "x dt ids t w T v K N re scale gs loss sum lse d gdt st stream",
-                         (P, 1, P, P, None, 4, 300, 8, 2, 1, 1.0, 1.0, P, P, None, None, 0, None,
-                          None), **k)
+                         "x dt ids t w T v K N re scale gs loss sum lse d gdt ws wsb st stream",
+                         (P, 1, P, P, None, 4, 300, 8, 2, 1, 1.0, 1.0, P, P, None, None, 0, P, 320,
+                          None, None), **k)
     assert f(x=None) == f(ids=None) == f(t=None) == f(loss=None) == NULL
     assert f(dt=3) == f(d=ctypes.c_void_p(1 << 21), gdt=9) == DTYPE
     assert f(K=0) == f(T=0) == f(v=0) == f(N=7) == f(scale=float("nan")) == SHAPE
     assert f(K=257) == UNSUPPORTED and f(d=P) == UNSUPPORTED
-    assert f(v=434178) == UNSUPPORTED and f(v=868354, dt=0) == UNSUPPORTED
-    assert f(x=ODD) == f(d=ODD) == ALIGN
+    assert f(v=337922) == UNSUPPORTED and f(v=337922, dt=0) == UNSUPPORTED
+    assert f(x=ODD) == f(d=ODD) == f(ws=ODD) == ALIGN
+    assert tpl.tp_workspace_bytes(tpl.OP_DISTILL, 4, 8, 300, 2) >= 4 * (16 + 8 * 8) == 320
+    assert f(ws=None) == f(wsb=319) == WORKSPACE
 
 
 def test_linear_logprobs_abi(L):
@@ -165,5 +167,5 @@ def test_linear_logprobs_abi(L):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a device answers instead")
 def test_no_device_no_fallback(L):
     assert L.vp_logprobs_fwd(P, 1, P, 4, 300, 2, 1.0, 0, P, P, P, None, None, None, None) == DEVICE
-    assert L.vp_distill(P, 1, P, P, None, 4, 300, 8, 2, 1, 1.0, 1.0, P, P, None, None, 0, None,
-                        None) == DEVICE
+    assert L.vp_distill(P, 1, P, P, None, 4, 300, 8, 2, 1, 1.0, 1.0, P, P, None, None, 0, P,
+                        320, None, None) == DEVICE
