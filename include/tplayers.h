@@ -640,8 +640,8 @@ TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t*
  *   temperature beforehand.)  A token listed twice counts twice.
  *
  *   logits [T,v] bf16 or fp32 (dt), dlogits grad_dt, both 16-byte aligned,
- *   any v up to 337920 (a row is held on chip by eight SMs); dlogits may be
- *   the logits themselves when grad_dt == dt and must not overlap them
+ *   any v, with dlogits up to 337920 (a row is held on chip by eight SMs);
+ *   dlogits may be the logits themselves when grad_dt == dt and must not overlap them
  *   otherwise.  1 <= K <= 256.  Longer rows and larger K return
  *   TP_ERR_UNSUPPORTED.  scale finite and > 0.  v % N == 0; no output depends on N.
  *   A row with w == 0, or without a filled slot of probability above 0, has

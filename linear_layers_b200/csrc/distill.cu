@@ -20,6 +20,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <type_traits>
 
 #include "internal.h"
 #include "rowwise.cuh"
@@ -76,113 +77,158 @@ struct Slots {
 };
 
 constexpr int kPrepWarps = 4;
-constexpr int kSlots = kDistillMaxK / 32;   // slots per lane
-constexpr int kSeenWords = 1024;            // 32768 bits to notice a token listed twice
 
-// One warp per row.  The sums run over the lanes' slots and then by shuffles,
-// the same order every time.
+// The teacher's probabilities of one row in one warp, slot lane + 32·i in
+// place i: ids with −1 for empty and bad slots and those of probability 0,
+// log p and p.  The sums run over the lanes' slots and then by shuffles, the
+// same order every time.
+template <int S>
+struct RowSlots {
+  int32_t id[S];
+  float lp[S], p[S];
+  float P, C;    // Σ p, Σ p·log p
+  bool bad;
+
+  __device__ __forceinline__ RowSlots(const DistillArgs& a, int64_t t, int lane) {
+    bad = false;
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int s = lane + 32 * i;
+      id[i] = -1;
+      lp[i] = -CUDART_INF_F;
+      if (s < a.K) {
+        id[i] = a.ids[t * a.K + s];
+        lp[i] = a.teacher[t * a.K + s];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const bool out = id[i] < -1 || id[i] >= a.v;
+      bad |= out;
+      if (out || id[i] == -1) {   // the value of an empty slot is not looked at
+        id[i] = -1;
+        lp[i] = -CUDART_INF_F;
+      }
+      top = fmaxf(top, lp[i]);
+    }
+    if (a.renormalize) {
+      top = warp_max(top);
+      if (top == -CUDART_INF_F) top = 0.0f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        lp[i] -= top;
+        sum += expf(lp[i]);
+      }
+      sum = warp_sum(sum);
+      const float log_sum = sum == 0.0f ? 0.0f : logf(sum);
+#pragma unroll
+      for (int i = 0; i < S; ++i) lp[i] -= log_sum;
+    }
+    P = C = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      p[i] = id[i] == -1 ? 0.0f : expf(lp[i]);
+      P += p[i];
+      if (p[i] != 0.0f) C = fmaf(p[i], lp[i], C);
+      else id[i] = -1;
+    }
+    P = warp_sum(P);
+    C = warp_sum(C);
+    bad = __any_sync(0xffffffffu, bad);
+  }
+};
+
+// One warp per row; S slots per lane.
+template <int S>
 __global__ void __launch_bounds__(kPrepWarps * 32)
     distill_slots_kernel(const DistillArgs a, int2* __restrict__ entries,
                          float4* __restrict__ info) {
+  constexpr int kSeenWords = 128 * S;   // 128 bits for every slot, to notice a token listed twice
   __shared__ uint32_t seen_bits[kPrepWarps][kSeenWords];
-  __shared__ int2 listed[kPrepWarps][kDistillMaxK];
+  __shared__ int2 listed[kPrepWarps][32 * S];
   grid_dependents_launch();   // the rows' kernel reads nothing of this one before it has ended
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepWarps + warp;
   if (t >= a.T) return;
   uint32_t* seen = seen_bits[warp];
-  for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
-  int32_t id[kSlots];
-  float lp[kSlots], p[kSlots];
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const int s = lane + 32 * i;
-    id[i] = -1;
-    lp[i] = -CUDART_INF_F;
-    if (s < a.K) {
-      id[i] = a.ids[t * a.K + s];
-      lp[i] = a.teacher[t * a.K + s];
-    }
-  }
-  bool bad = false;
-  float top = -CUDART_INF_F;
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const bool out = id[i] < -1 || id[i] >= a.v;
-    bad |= out;
-    if (out || id[i] == -1) {   // the value of an empty slot is not looked at
-      id[i] = -1;
-      lp[i] = -CUDART_INF_F;
-    }
-    top = fmaxf(top, lp[i]);
-  }
-  if (a.renormalize) {
-    top = warp_max(top);
-    if (top == -CUDART_INF_F) top = 0.0f;
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      lp[i] -= top;
-      sum += expf(lp[i]);
-    }
-    sum = warp_sum(sum);
-    const float log_sum = sum == 0.0f ? 0.0f : logf(sum);
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) lp[i] -= log_sum;
-  }
-  float P = 0.0f, C = 0.0f;
+  for (int i = 0; i < S; ++i)
+    reinterpret_cast<uint4*>(seen)[lane + 32 * i] = make_uint4(0, 0, 0, 0);
+  RowSlots<S> r(a, t, lane);
   __syncwarp();
   uint32_t again = 0;   // bit i: another slot had the bit of slot i's token
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    p[i] = id[i] == -1 ? 0.0f : expf(lp[i]);
-    P += p[i];
-    if (p[i] != 0.0f) C = fmaf(p[i], lp[i], C);
-    else id[i] = -1;
-    if (id[i] >= 0) {
-      const uint32_t bit = static_cast<uint32_t>(id[i]) & (kSeenWords * 32 - 1);
+  for (int i = 0; i < S; ++i)
+    if (r.id[i] >= 0) {
+      const uint32_t bit = static_cast<uint32_t>(r.id[i]) & (kSeenWords * 32 - 1);
       again |= ((atomicOr(&seen[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u) << i;
     }
-  }
   if (__any_sync(0xffffffffu, again)) {
     // a token twice, or two tokens on one bit: looked up, slot group by slot group
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      listed[warp][lane + 32 * i] = make_int2(id[i], __float_as_int(p[i]));
+    for (int i = 0; i < S; ++i)
+      listed[warp][lane + 32 * i] = make_int2(r.id[i], __float_as_int(r.p[i]));
     __syncwarp();
     bool twice = false;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (__any_sync(0xffffffffu, (again >> i) & 1u))
-        for (int q = 0; q < a.K; ++q)
-          twice |= id[i] >= 0 && listed[warp][q].x == id[i] && q != lane + 32 * i;
+    for (int i = 0; i < S; ++i)
+      if (__any_sync(0xffffffffu, (again >> i) & 1u)) {
+#pragma unroll 8
+        for (int q = 0; q < 32 * S; ++q)
+          twice |= r.id[i] >= 0 && listed[warp][q].x == r.id[i] && q != lane + 32 * i;
+      }
     if (__any_sync(0xffffffffu, twice)) {
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (32 * i >= a.K) break;
+      for (int i = 0; i < S; ++i) {
         float sum = 0.0f;
         bool first = true;
-        for (int q = 0; q < a.K; ++q) {   // in slot order
+#pragma unroll 8
+        for (int q = 0; q < 32 * S; ++q) {   // in slot order
           const int2 e = listed[warp][q];
-          if (e.x == id[i]) {
+          if (e.x == r.id[i]) {
             if (q < lane + 32 * i) first = false;
             sum += __int_as_float(e.y);
           }
         }
-        p[i] = sum;
-        if (!first) id[i] = -1;
+        r.p[i] = sum;
+        if (!first) r.id[i] = -1;
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i)
+  for (int i = 0; i < S; ++i)
     if (lane + 32 * i < a.K)
-      entries[t * a.K + lane + 32 * i] = make_int2(id[i], __float_as_int(p[i]));
-  P = warp_sum(P);
-  C = warp_sum(C);
-  bad = __any_sync(0xffffffffu, bad);
+      entries[t * a.K + lane + 32 * i] = make_int2(r.id[i], __float_as_int(r.p[i]));
   if (lane == 0)
-    info[t] = make_float4(P, C, bad ? 1.0f : 0.0f, a.weight ? a.weight[t] : 1.0f);
+    info[t] = make_float4(r.P, r.C, r.bad ? 1.0f : 0.0f, a.weight ? a.weight[t] : 1.0f);
+}
+
+// Without a gradient the logits are needed once: the rows' sums come from the
+// log-probability kernel (sums [T] of (r, log S)), and one warp per row gathers
+// the listed logits.
+template <typename IT, int S>
+__global__ void __launch_bounds__(kPrepWarps * 32)
+    distill_loss_kernel(const DistillArgs a, const float2* __restrict__ sums) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const RowSlots<S> r(a, t, lane);
+  const float2 rs = sums[t];
+  float A = 0.0f;
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    if (r.id[i] >= 0)
+      A = fmaf(r.p[i], to_f32(static_cast<const IT*>(a.logits)[t * a.v + r.id[i]]) - rs.x, A);
+  A = warp_sum(A);
+  if (lane == 0) {
+    const float w = a.weight ? a.weight[t] : 1.0f;
+    const bool dead = w == 0.0f || (r.P == 0.0f && !r.bad);
+    const float loss = fmaf(r.P, rs.y, fmaf(-a.scale, A, r.C));
+    a.loss[t] = dead ? 0.0f : r.bad ? CUDART_NAN_F : w * loss;
+    if (!dead && r.bad && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -462,17 +508,15 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
           if (!dead && any_bad && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
         }
       }
-      if (a.dlogits != nullptr) {
-        named_barrier_sync(2, NT + 32);   // P·q is written
-        if (!dead) {
-          const float c = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale;
-          const float inv = 1.0f / all.s;
-          GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
+      named_barrier_sync(2, NT + 32);   // P·q is written
+      if (!dead) {
+        const float c = any_bad ? CUDART_NAN_F : a.grad_scale * w * a.scale;
+        const float inv = 1.0f / all.s;
+        GT* out = static_cast<GT*>(a.dlogits) + t * a.v;
 #pragma unroll 4
-          for (int e = lane; e < n; e += 32)
-            put(out + own[e].x, c * (P * (ex2_approx((own_x[e] - ref) * sl) * inv) -
-                                     __int_as_float(own[e].y)));
-        }
+        for (int e = lane; e < n; e += 32)
+          put(out + own[e].x, c * (P * (ex2_approx((own_x[e] - ref) * sl) * inv) -
+                                   __int_as_float(own[e].y)));
       }
       n = n_next;
     }
@@ -551,7 +595,6 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
                       0.0f);
       }
       const Sums all = row_sums(k);
-      if (a.dlogits == nullptr) continue;
       const float ref = all.m == -CUDART_INF_F ? 0.0f : all.m;
       const float4 info = row_info[par];
       const float P = info.x, w = info.w;
@@ -678,20 +721,55 @@ tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_
 
 }  // namespace
 
+namespace {
+
+// f(slots per lane) for K slots
+template <typename F>
+void with_slots(int K, F f) {
+  if (K <= 32) f(std::integral_constant<int, 1>());
+  else if (K <= 64) f(std::integral_constant<int, 2>());
+  else if (K <= 128) f(std::integral_constant<int, 4>());
+  else f(std::integral_constant<int, 8>());
+}
+
+}  // namespace
+
 size_t distill_ws_bytes(int64_t T, int64_t K) {
   return static_cast<size_t>(T) * (sizeof(float4) + K * sizeof(int2));
 }
 
 tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, float* loss_sum,
                          void* ws, cudaStream_t stream) {
+  static_assert(kDistillMaxK <= 8 * 32, "slots of a row in one warp");
+  const unsigned prep = static_cast<unsigned>((a.T + kPrepWarps - 1) / kPrepWarps);
+  if (a.dlogits == nullptr) {
+    LogprobsArgs l = {};
+    l.logits = a.logits;
+    l.T = a.T;
+    l.v = a.v;
+    l.scale = a.scale;
+    l.lse = a.lse;
+    l.sums = static_cast<float2*>(ws);
+    if (tp_status st = logprobs_fwd_launch(l, dt, stream)) return st;
+    with_slots(a.K, [&](auto s) {
+      if (dt == TP_DTYPE_BF16)
+        distill_loss_kernel<__nv_bfloat16, s()><<<prep, kPrepWarps * 32, 0, stream>>>(a, l.sums);
+      else
+        distill_loss_kernel<float, s()><<<prep, kPrepWarps * 32, 0, stream>>>(a, l.sums);
+    });
+    note_launches(1);
+    if (cudaGetLastError() != cudaSuccess) return TP_ERR_CUDA;
+    return loss_sum ? loss_sum_launch(a.loss, a.T, loss_sum, stream) : TP_OK;
+  }
   float4* info = static_cast<float4*>(ws);
   int2* entries = reinterpret_cast<int2*>(info + a.T);
-  distill_slots_kernel<<<static_cast<unsigned>((a.T + kPrepWarps - 1) / kPrepWarps),
-                         kPrepWarps * 32, 0, stream>>>(a, entries, info);
+  with_slots(a.K, [&](auto s) {
+    distill_slots_kernel<s()><<<prep, kPrepWarps * 32, 0, stream>>>(a, entries, info);
+  });
   note_launches(1);
   if (cudaGetLastError() != cudaSuccess) return TP_ERR_CUDA;
   const Slots slots{entries, info};
-  const bool f32_grad = a.dlogits && grad_dt == TP_DTYPE_F32;
+  const bool f32_grad = grad_dt == TP_DTYPE_F32;
   tp_status st;
   if (dt == TP_DTYPE_BF16)
     st = f32_grad ? distill_launch_t<__nv_bfloat16, float>(a, slots, stream)

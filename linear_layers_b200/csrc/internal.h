@@ -153,6 +153,7 @@ struct LogprobsArgs {
   int32_t* top_idx;         // [T, top_k]
   float* top_logprob;
   int32_t* dev_status;
+  float2* sums;             // [T] (r, log S) with lse = scale·r + log S; nullable
 };
 struct LogprobsBwdArgs {
   const void* logits;
@@ -177,7 +178,8 @@ tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_
 
 // Distillation from a teacher's top entries: see vp_distill.
 constexpr int kDistillMaxK = 256;
-// The widest row: eight blocks of 480 threads hold 88 logits a thread.
+// The widest row of a gradient: eight blocks of 480 threads hold 88 logits a
+// thread.
 constexpr int64_t kDistillMaxV = 8 * 480 * 88;
 struct DistillArgs {
   const void* logits;

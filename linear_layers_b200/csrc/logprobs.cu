@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
   if (tid == 0) {
     if (a.entropy) a.entropy[t] = log_s - a.scale * (all.u / all.s);
     if (a.lse) a.lse[t] = fmaf(a.scale, ref, log_s);
+    if (a.sums) a.sums[t] = make_float2(ref, log_s);
   }
   if constexpr (kTop)
     ranked(cand.n, [&](int i, uint64_t q) {

@@ -827,7 +827,7 @@ tp_status vp_logprobs_fwd(const void* logits, tp_dtype dt, const int64_t* target
     return TP_ERR_ALIGN;
   if (tp_status s = require_sm100()) return s;
   LogprobsArgs a{logits, targets, T,   v,       scale,       top_k,
-                 logprob, entropy, lse, top_idx, top_logprob, dev_status};
+                 logprob, entropy, lse, top_idx, top_logprob, dev_status, nullptr};
   return logprobs_fwd_launch(a, dt, as_stream(stream));
 }
 
@@ -858,7 +858,7 @@ tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids
   if (!logits || !teacher_ids || !teacher_logits || !loss) return TP_ERR_NULL;
   if (!dtype_ok(dt) || (dlogits && !dtype_ok(grad_dt))) return TP_ERR_DTYPE;
   if (!dims_ok({T, v, K}) || N < 1 || v % N || !scale_ok(scale)) return TP_ERR_SHAPE;
-  if (K > kDistillMaxK || v > kDistillMaxV) return TP_ERR_UNSUPPORTED;
+  if (K > kDistillMaxK || (dlogits && v > kDistillMaxV)) return TP_ERR_UNSUPPORTED;
   if (!ptrs_aligned({logits, dlogits, ws}) ||
       !words_aligned({teacher_ids, teacher_logits, weight, loss, loss_sum, lse}, 4))
     return TP_ERR_ALIGN;

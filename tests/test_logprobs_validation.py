@@ -140,7 +140,8 @@ def test_distill_abi(L):
     assert f(dt=3) == f(d=ctypes.c_void_p(1 << 21), gdt=9) == DTYPE
     assert f(K=0) == f(T=0) == f(v=0) == f(N=7) == f(scale=float("nan")) == SHAPE
     assert f(K=257) == UNSUPPORTED and f(d=P) == UNSUPPORTED
-    assert f(v=337922) == UNSUPPORTED and f(v=337922, dt=0) == UNSUPPORTED
+    D = ctypes.c_void_p(1 << 21)
+    assert f(v=337922, d=D) == UNSUPPORTED and f(v=337922, dt=0, d=D) == UNSUPPORTED
     assert f(x=ODD) == f(d=ODD) == f(ws=ODD) == ALIGN
     assert tpl.tp_workspace_bytes(tpl.OP_DISTILL, 4, 8, 300, 2) >= 4 * (16 + 8 * 8) == 320
     assert f(ws=None) == f(wsb=319) == WORKSPACE
