@@ -140,13 +140,13 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()   # an int: the argument types make it a pointer
 
 
 def _stream(device):
     if torch.device(device).type != "cuda":
         raise RuntimeError("linear_layers_b200 runs on CUDA tensors only; there is no CPU path")
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -188,7 +188,8 @@ def _want(dev, *specs):
             raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, the operands on {dev}")
-        if shape is not None and tuple(t.shape) != tuple(int(x) for x in shape):
+        if (shape is not None and t.shape != shape
+                and tuple(t.shape) != tuple(int(x) for x in shape)):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
@@ -688,6 +689,13 @@ def tp_attention_bwd(QKV, ctx, dctx, lse, b, s, n_heads, N, *, head_offsets=None
     return dQKV
 
 
+def _row_outputs(T, dev, *given):
+    """The given fp32 [T] outputs, the missing ones from one allocation."""
+    if all(g is None for g in given):
+        return torch.empty(len(given), T, dtype=torch.float32, device=dev).unbind(0)
+    return [torch.empty(T, dtype=torch.float32, device=dev) if g is None else g for g in given]
+
+
 def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, entropy=None,
                     lse=None, top_idx=None, top_logprob=None, dev_status=None):
     """Log-probability of targets[t] (None: left out), entropy, log-sum-exp and the top_k
@@ -699,10 +707,10 @@ def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, ent
     dev = logits.device
     if targets is None and logprob is not None:
         raise ValueError("logprob needs targets")
-    if logprob is None and targets is not None:
-        logprob = torch.empty(T, dtype=torch.float32, device=dev)
-    entropy = torch.empty(T, dtype=torch.float32, device=dev) if entropy is None else entropy
-    lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
+    if targets is None:
+        entropy, lse = _row_outputs(T, dev, entropy, lse)
+    else:
+        logprob, entropy, lse = _row_outputs(T, dev, logprob, entropy, lse)
     if top_k > 0:
         if top_idx is None:
             top_idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
@@ -722,14 +730,20 @@ def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, ent
             "top_logprob": top_logprob}
 
 
+# The current stream's handle without a Stream object: a third of a small call's host time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(fn, dev, *args):
     """fn(*args, stream) on dev's current stream, with dev current during the call (the library
     launches on the current device)."""
-    stream = _stream(dev)
+    if dev.type != "cuda":
+        _stream(dev)   # raises
     if dev.index == torch.cuda.current_device():
-        return fn(*args, stream)
+        return fn(*args, _raw_stream(dev.index))
     with torch.cuda.device(dev):
-        return fn(*args, stream)
+        return fn(*args, _raw_stream(dev.index))
 
 
 def _logprob_grad_args(targets, entropy, dlogprob, dentropy):
@@ -774,9 +788,8 @@ def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weig
     T, v = logits.shape
     dev = logits.device
     K = teacher_ids.shape[1]
-    loss = torch.empty(T, dtype=torch.float32, device=dev) if loss is None else loss
+    loss, lse = _row_outputs(T, dev, loss, lse)
     loss_sum = torch.empty(1, dtype=torch.float32, device=dev) if loss_sum is None else loss_sum
-    lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
     if with_grad and dlogits is None:
         dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
     _contig(logits, teacher_ids, teacher_logits, weight, loss, loss_sum, lse, dlogits)
@@ -802,10 +815,10 @@ def tp_linear_logprobs_fwd(H, E, targets, N, *, scale=1.0, logprob=None, entropy
     dev = H.device
     if targets is None and logprob is not None:
         raise ValueError("logprob needs targets")
-    if logprob is None and targets is not None:
-        logprob = torch.empty(T, dtype=torch.float32, device=dev)
-    entropy = torch.empty(T, dtype=torch.float32, device=dev) if entropy is None else entropy
-    lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
+    if targets is None:
+        entropy, lse = _row_outputs(T, dev, entropy, lse)
+    else:
+        logprob, entropy, lse = _row_outputs(T, dev, logprob, entropy, lse)
     _contig(H, E, targets, logprob, entropy, lse)
     _want(dev, ("H", H, (T, h), _BF), ("E", E, (v, h), _BF), ("targets", targets, (T,), _I64T),
           ("logprob", logprob, (T,), _F32), ("entropy", entropy, (T,), _F32),
