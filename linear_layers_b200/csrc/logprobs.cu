@@ -22,8 +22,11 @@
 namespace tpl {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;       // of a forward block
 constexpr int kWarps = kThreads / 32;
+constexpr int kBwdThreads = 256;    // of a gradient block, and of the slices' combine
+constexpr int kBwdWarps = kBwdThreads / 32;
+
 // ---------------------------------------------------------------------------
 // top alternatives
 // ---------------------------------------------------------------------------
@@ -34,6 +37,7 @@ __device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
   const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   return (static_cast<uint64_t>(o) << 32) | (0xffffffffu - index);
 }
+constexpr uint32_t kBehind = 0x40000001u;   // behind every index
 __device__ __forceinline__ float key_value(uint64_t key) {
   const uint32_t o = static_cast<uint32_t>(key >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
@@ -42,46 +46,55 @@ __device__ __forceinline__ int32_t key_index(uint64_t key) {
   return static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key));
 }
 
-// The r-th largest of the warp's keys (distinct but for 0), 0 if there are fewer.
-__device__ __forceinline__ uint64_t warp_rth_key(uint64_t key, int r) {
+// The r-th largest of the warp's keys, two per lane (key >= second; distinct but
+// for 0), 0 if there are fewer.
+__device__ __forceinline__ uint64_t warp_rth_key(uint64_t key, uint64_t second, int r) {
   uint64_t best = 0;
   for (int i = 0; i < r; ++i) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
     const uint32_t lo = __reduce_max_sync(
         0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
     best = (static_cast<uint64_t>(hi) << 32) | lo;
-    if (key == best) key = 0;
+    if (key == best) {
+      key = second;
+      second = 0;
+    }
   }
   return best;
 }
 
 // The row's top k, exactly, from one streaming pass.  While a block adds up
-// its range it only notes the maximum of each thread's elements in each of
-// (up to) kGroups stretches of the range.  Then
-//   - the threshold: the smallest over the warps of the ceil(k/8)-th largest
-//     of the lanes' maxima, a key that at least k elements reach;
+// its range it notes the maximum of every group, the elements of one thread in
+// one or few steps.  Then
+//   - the threshold: the smallest over the warps of the ceil(k/4)-th largest
+//     of their lanes' two largest maxima, a key that at least k elements reach;
 //   - the groups whose maximum reaches it (about 1.5·k of them) are read again
-//     from L2 and their elements at or above the threshold become candidates;
-//   - if more than kLimit candidates have gathered (equal or ordered values),
-//     the threshold is raised among them and the rest dropped.  The buffer has
-//     room for kLimit and one more step of the whole block: it cannot overflow.
-// Gathering while streaming instead, against a threshold from the first
-// elements, cost 33 instructions per element of a v=50304 row at k = 64.
-template <int kStep>
+//     and their elements at or above the threshold become candidates;
+//   - the candidates are placed by counting.
+// If more elements reach the threshold than the buffer holds (equal values),
+// the range is read once more in barrier-separated steps, and whenever kLimit
+// candidates have gathered the threshold is raised among them and the rest
+// dropped.
+// 8192 bf16 rows of 50304 take 141 us without alternatives, 190 at k = 1, 241 at
+// k = 64, 319 at k = 128: the instructions behind a row's last load.  Gathering while streaming, against a threshold from the first
+// elements, took twice the instructions.
 struct Candidates {
   static constexpr int kLimit = 512;
-  static constexpr int kRoom = kLimit + kStep + 16;
-  static constexpr int kGroups = 16;
+  static constexpr int kRoom = kLimit + kThreads * 8 + 16;   // kLimit and a step of units
+  static constexpr int kGroups = 32;
+  static constexpr int kHits = 1024;
   uint64_t key[kRoom];
   uint64_t warp_key[kWarps];
   uint64_t kth;
-  float group_max[kGroups][kThreads];
-  uint16_t hit[kGroups * kThreads];
-  int n, kept, hits;
+  int n, kept;
+  int hits;
+  uint16_t hit[kHits];
+  alignas(16) float4 group_max[];   // [groups / 4][kThreads], four groups each
 
-  // Smallest over the warps of the r-th largest key held by their lanes.
-  __device__ __forceinline__ uint64_t threshold(uint64_t lane_key, int k) {
-    const uint64_t w = warp_rth_key(lane_key, (k + kWarps - 1) / kWarps);
+  // Smallest over the warps of the ceil(k / kWarps)-th largest of the keys held
+  // by their lanes, two each (a >= b).
+  __device__ __forceinline__ uint64_t threshold(uint64_t key_a, uint64_t key_b, int k) {
+    const uint64_t w = warp_rth_key(key_a, key_b, (k + kWarps - 1) / kWarps);
     if ((threadIdx.x & 31) == 0) warp_key[threadIdx.x >> 5] = w;
     __syncthreads();
     uint64_t t = warp_key[0];
@@ -110,14 +123,18 @@ struct Candidates {
   // Fewer candidates, the top k among them; raises t.  All threads, after a
   // barrier; ends with one.
   __device__ __forceinline__ int shrink(int count, int k, uint64_t& t) {
-    uint64_t best = 0;
-    for (int i = threadIdx.x; i < count; i += kThreads) best = best > key[i] ? best : key[i];
-    const uint64_t low = threshold(best, k);
+    uint64_t best = 0, second = 0;
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const uint64_t q = key[i];
+      second = q > best ? best : q > second ? q : second;
+      best = q > best ? q : best;
+    }
+    const uint64_t low = threshold(best, second, k);
     if (low > t) t = low;
     const uint64_t floor_key = t;
     return compact(count, [=](int, uint64_t q) { return q >= floor_key; });
   }
-  // The same down to k exactly (count² / 256 comparisons a thread): for
+  // The same down to k exactly (count² / kThreads comparisons a thread): for
   // orders of values that the threshold does not thin out.
   __device__ __forceinline__ int shrink_exact(int count, int k, uint64_t& t) {
     uint32_t flags = 0;
@@ -136,18 +153,23 @@ struct Candidates {
   }
 };
 
+// Units per thread and step: with alternatives fewer threads are on an SM, and
+// each keeps more bytes in flight.
+constexpr int step_units(bool top) { return top ? 4 : 2; }
+
 // Log-probability statistics of one row by `slices` blocks (a cluster), each
 // taking a contiguous range of the row's 16-byte units.  A block streams its
 // range with the next step's loads in flight while it adds up the present
 // one; sums and candidates of the blocks meet in block 0 through distributed
-// shared memory.  Reading the row once is the bound: 256 threads hold 64 bytes
-// each in flight.
+// shared memory.  Reading the row once is the bound for fp32 logits (8192 rows
+// of 50304: 246 us, 6.7 TB/s); bf16 ones take as many instructions for half the
+// bytes (141 us, 5.8 TB/s).
 template <typename IT, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
+__global__ void __launch_bounds__(kThreads, kTop ? (Unit<IT>::kN == 4 ? 8 : 7) : 10)
     logprobs_kernel(const LogprobsArgs a, int slices) {
   constexpr int kN = Unit<IT>::kN;
-  constexpr int kUnits = 2;                       // units per thread and step
-  using Cand = Candidates<kTop ? kThreads * kN : 0>;
+  constexpr int kUnits = step_units(kTop);
+  using Cand = Candidates;
   extern __shared__ __align__(16) uint8_t dyn_smem[];
   Cand& cand = *reinterpret_cast<Cand*>(dyn_smem);   // only touched with kTop
   __shared__ Sums wsum[kWarps];
@@ -178,10 +200,14 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
   const uint4 fill = make_uint4(Unit<IT>::kMinusInf, Unit<IT>::kMinusInf, Unit<IT>::kMinusInf,
                                 Unit<IT>::kMinusInf);
   auto load = [&](int base, uint4 (&w)[kUnits]) {
+    const IT* p = body + static_cast<int64_t>(base + tid) * kN;
+    if (base + kThreads * kUnits <= u1) {
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int u = base + i * kThreads + tid;
-      w[i] = u < u1 ? ld_unit(body + static_cast<int64_t>(u) * kN) : fill;
+      for (int i = 0; i < kUnits; ++i) w[i] = ld_unit(p + i * kThreads * kN);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+        w[i] = base + i * kThreads + tid < u1 ? ld_unit(p + i * kThreads * kN) : fill;
     }
   };
   // position in the row of unit u's first element
@@ -191,32 +217,32 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
   uint4 next[kUnits];
   load(u0, next);
   const int steps = (u1 - u0 + kThreads * kUnits - 1) / (kThreads * kUnits);
-  // steps per group, the group being filled, the lane's maximum and the last
-  // position it can have (equal maxima: the first step's)
-  [[maybe_unused]] const int group_steps = (steps + Cand::kGroups - 1) / Cand::kGroups;
-  [[maybe_unused]] int group = 0, group_left = group_steps, lane_step = 0;
-  [[maybe_unused]] float group_mx = -CUDART_INF_F, lane_mx = -CUDART_INF_F;
-  [[maybe_unused]] bool lane_has = false;
-  for (int st = 0; st < steps; ++st) {
-    const int base = u0 + st * kThreads * kUnits;
-    float x[kUnits * kN];
+  // groups of 2^group_log steps, at most kGroups of them
+  int group_log = 0;
+  if constexpr (kTop)
+    while ((Cand::kGroups << group_log) < steps) ++group_log;
+  const int group_steps = kTop ? 1 << group_log : max(steps, 1);
+  const int groups = kTop ? (steps + group_steps - 1) >> group_log : min(steps, 1);
+  [[maybe_unused]] bool lane_has = false;   // the lane's first element is there and a number
+  if constexpr (kTop) {
+    float x[kN];
+    Unit<IT>::unpack(next[0], x);
+    lane_has = u0 + tid < u1 && x[0] == x[0];
+  }
+  int st = 0;
+  for (int g = 0; g < groups; ++g) {
+    [[maybe_unused]] float group_mx = -CUDART_INF_F;
+    const int end = min(st + group_steps, steps);
+    for (; st < end; ++st) {
+      float x[kUnits * kN];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) Unit<IT>::unpack(next[i], x + i * kN);
-    if (st + 1 < steps) load(base + kThreads * kUnits, next);
-    const float mx = sums.add<kUnits * kN, true>(x, sl, tau);
-    if constexpr (kTop) {
-      if (st == 0) lane_has = u0 + tid < u1 && x[0] == x[0];
-      if (mx > lane_mx) {
-        lane_mx = mx;
-        lane_step = st;
-      }
-      group_mx = fmaxf(group_mx, mx);
-      if (--group_left == 0 || st + 1 == steps) {
-        cand.group_max[group++][tid] = group_mx;
-        group_mx = -CUDART_INF_F;
-        group_left = group_steps;
-      }
+      for (int i = 0; i < kUnits; ++i) Unit<IT>::unpack(next[i], x + i * kN);
+      if (st + 1 < steps) load(u0 + (st + 1) * kThreads * kUnits, next);
+      const float mx = sums.add<kUnits * kN, true>(x, sl, tau);
+      if constexpr (kTop) group_mx = fmaxf(group_mx, mx);
     }
+    if constexpr (kTop)
+      reinterpret_cast<float*>(&cand.group_max[(g >> 2) * kThreads + tid])[g & 3] = group_mx;
   }
   // the edges of the row: at most kN − 1 elements at each end
   int edge_j = -1;
@@ -230,58 +256,133 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
   }
 
   if constexpr (kTop) {
-    bool full = false;   // a candidate landed at or past kLimit
-    auto admit = [&](uint64_t q) {
-      const int at = atomicAdd(&cand.n, 1);
-      cand.key[at] = q;
-      full |= at >= Cand::kLimit;
-    };
     if (tid == 0) cand.n = cand.hits = 0;
-    // A lane's key may place its maximum too late, never too early.  A lane
-    // of nothing but −inf (or NaN) has its first element, if that is −inf.
-    uint64_t lane_key = 0;
-    if (lane_mx > -CUDART_INF_F)
-      lane_key = rank_key(lane_mx, first_of(u0 + (lane_step * kUnits + kUnits - 1) * kThreads + tid) + kN - 1);
+    // what the last four groups have of places without a group
+    for (int g = groups; g & 3; ++g)
+      reinterpret_cast<float*>(&cand.group_max[(g >> 2) * kThreads + tid])[g & 3] = -CUDART_INF_F;
+    const int quads = (groups + 3) >> 2;
+    float mx_a = -CUDART_INF_F, mx_b = -CUDART_INF_F;   // the lane's two largest maxima
+    auto with_max = [&](float gm) {
+      mx_b = fmaxf(mx_b, fminf(mx_a, gm));
+      mx_a = fmaxf(mx_a, gm);
+    };
+    for (int q = 0; q < quads; ++q) {
+      const float4 m4 = cand.group_max[q * kThreads + tid];
+      with_max(m4.x);
+      with_max(m4.y);
+      with_max(m4.z);
+      with_max(m4.w);
+    }
+    // The keys place the maxima behind every element of the row (a threshold
+    // may be low, never high), apart from each other.  A lane of nothing but
+    // −inf (or NaN) has its first element, if that is −inf.
+    uint64_t key_a = 0, key_b = 0;
+    if (mx_a > -CUDART_INF_F)
+      key_a = rank_key(mx_a, kBehind + 2 * tid);
     else if (lane_has)
-      lane_key = rank_key(-CUDART_INF_F, first_of(u0 + tid));
-    uint64_t floor_key = cand.threshold(lane_key, a.top_k);   // a barrier within
-    for (int g = 0; g < group; ++g) {
-      const uint32_t at = first_of(u0 + g * group_steps * kUnits * kThreads + tid);
-      if (rank_key(cand.group_max[g][tid], at) >= floor_key)
-        cand.hit[atomicAdd(&cand.hits, 1)] = static_cast<uint16_t>(g * kThreads + tid);
-    }
-    if (edge_j >= 0 && edge_x == edge_x) {
-      const uint64_t q = rank_key(edge_x, static_cast<uint32_t>(edge_j));
-      if (q >= floor_key) admit(q);
-    }
-    __syncthreads();
-    // one unit of a hit group per thread and round
-    const int group_units = group_steps * kUnits;
-    const int items = cand.hits * group_units;
-    for (int base = 0; base < items; base += kThreads) {
-      const int item = base + tid;
-      if (item < items) {
-        const int h = cand.hit[item / group_units];
-        const int u = u0 + ((h / kThreads) * group_units + item % group_units) * kThreads +
-                      h % kThreads;
-        if (u < u1) {
-          float x[kN];
-          Unit<IT>::unpack(*reinterpret_cast<const uint4*>(body + static_cast<int64_t>(u) * kN), x);
-          const float floor_x = floor_key ? key_value(floor_key) : -CUDART_INF_F;
+      key_a = rank_key(-CUDART_INF_F, first_of(u0 + tid));
+    if (mx_b > -CUDART_INF_F) key_b = rank_key(mx_b, kBehind + 2 * tid + 1);
+    uint64_t floor_key = cand.threshold(key_a, key_b, a.top_k);   // a barrier within
+    // a place in a list of the block for each of the warp's lanes' n entries
+    auto places = [&](int n, int* total) {
+      int upto = n;
 #pragma unroll
-          for (int i = 0; i < kN; ++i)
-            if (x[i] >= floor_x) {   // not NaN
-              const uint64_t q = rank_key(x[i], first_of(u) + i);
-              if (q >= floor_key) admit(q);
-            }
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, off);
+        if ((tid & 31) >= off) upto += o;
+      }
+      int base = 0;
+      if ((tid & 31) == 31 && upto) base = atomicAdd(total, upto);
+      return __shfl_sync(0xffffffffu, base, 31) + upto - n;
+    };
+    auto fetch = [&](int u) {
+      return u < u1 ? *reinterpret_cast<const uint4*>(body + static_cast<int64_t>(u) * kN) : fill;
+    };
+    auto admit_edge = [&]() {
+      if (edge_j >= 0 && edge_x == edge_x) {
+        const uint64_t q = rank_key(edge_x, static_cast<uint32_t>(edge_j));
+        if (q >= floor_key) cand.key[atomicAdd(&cand.n, 1)] = q;   // the first few places
+      }
+    };
+    admit_edge();
+    const float floor_x = floor_key ? key_value(floor_key) : -CUDART_INF_F;
+    const uint32_t floor_at = static_cast<uint32_t>(key_index(floor_key));
+    if (floor_key) {
+      uint32_t hits = 0;   // bit g: group g of this thread reaches it
+      for (int q = 0; q < quads; ++q) {
+        const float4 m4 = cand.group_max[q * kThreads + tid];
+        hits |= ((m4.x >= floor_x ? 1u : 0u) | (m4.y >= floor_x ? 2u : 0u) |
+                 (m4.z >= floor_x ? 4u : 0u) | (m4.w >= floor_x ? 8u : 0u)) << (4 * q);
+      }
+      if (floor_x == -CUDART_INF_F) {
+        // few elements above −inf, and the first ones of −inf: of the groups of
+        // nothing else only those that begin no later than the threshold's place
+        for (uint32_t h = hits; h; h &= h - 1) {
+          const int g = __ffs(h) - 1;
+          if (reinterpret_cast<const float*>(&cand.group_max[(g >> 2) * kThreads + tid])[g & 3] == floor_x &&
+              first_of(u0 + g * group_steps * kUnits * kThreads + tid) > floor_at)
+            hits &= ~(1u << g);
         }
       }
-      if (__syncthreads_or(full)) {
-        int left = cand.shrink(cand.n, a.top_k, floor_key);
-        if (left > Cand::kLimit / 2) left = cand.shrink_exact(left, a.top_k, floor_key);
-        full = false;
-        if (tid == 0) cand.n = left;
-        __syncthreads();
+      for (int at = places(__popc(hits), &cand.hits); hits; hits &= hits - 1, ++at)
+        if (at < Cand::kHits)
+          cand.hit[at] = static_cast<uint16_t>((__ffs(hits) - 1) * kThreads + tid);
+      __syncthreads();
+      // one unit of a hit group per thread
+      const int group_units = group_steps * kUnits;
+      const int items = min(cand.hits, Cand::kHits) * group_units;
+      for (int first = tid & ~31; first < items; first += kThreads) {   // warp by warp
+        const int item = first + (tid & 31);
+        int u = u1;
+        if (item < items) {
+          const int h = cand.hit[item / kUnits >> group_log];
+          u = u0 + ((h / kThreads) * group_units + (item & (group_units - 1))) * kThreads + h % kThreads;
+        }
+        float x[kN];
+        Unit<IT>::unpack(fetch(u), x);
+        // above the threshold's value, or equal and no later
+        const uint32_t first_at = u < u1 ? first_of(u) : 0xffffff00u;
+        uint32_t take = 0;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (x[i] > floor_x || (x[i] == floor_x && first_at + i <= floor_at)) take |= 1u << i;
+        int at = places(__popc(take), &cand.n);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if ((take >> i) & 1u) {
+            if (at < Cand::kRoom) cand.key[at] = rank_key(x[i], first_at + i);
+            ++at;
+          }
+      }
+    }
+    __syncthreads();
+    if (!floor_key || cand.n > Cand::kRoom || cand.hits > Cand::kHits) {
+      // fewer lanes with elements than a threshold needs, or more elements
+      // that reach it than there is room for: the whole range again, step by
+      // step, by value and place
+      __syncthreads();
+      if (tid == 0) cand.n = 0;
+      __syncthreads();
+      admit_edge();
+      __syncthreads();
+      for (int base = u0; base < u1; base += kThreads) {
+        const int u = base + tid;
+        float x[kN];
+        Unit<IT>::unpack(fetch(u), x);
+        uint32_t take = 0;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (u < u1 && x[i] == x[i] && rank_key(x[i], first_of(u) + i) >= floor_key) take |= 1u << i;
+        int at = places(__popc(take), &cand.n);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if ((take >> i) & 1u) cand.key[at++] = rank_key(x[i], first_of(u) + i);
+        if (__syncthreads_or(at > Cand::kLimit)) {
+          int left = cand.shrink(cand.n, a.top_k, floor_key);
+          if (left > Cand::kLimit / 2) left = cand.shrink_exact(left, a.top_k, floor_key);
+          if (tid == 0) cand.n = left;
+          __syncthreads();
+        }
       }
     }
   }
@@ -291,15 +392,21 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
   __syncthreads();
   Sums all = join_sums(kWarps, wsum[min(tid & 31, kWarps - 1)], sl);
 
-  // this block's best: a count of the candidates, rank by rank
+  // the top k of the n candidates, each placed by how many lie above it
   [[maybe_unused]] auto ranked = [&](int n, auto&& out) {
     if constexpr (kTop) {
       uint64_t floor_key = 0;
-      if (n > 2 * a.top_k + 64) n = cand.shrink(n, a.top_k, floor_key);
+      if (n > 3 * a.top_k + 64) n = cand.shrink(n, a.top_k, floor_key);
       for (int i = tid; i < n; i += kThreads) {
         const uint64_t q = cand.key[i];
         int rank_of = 0;
-        for (int j = 0; j < n; ++j) rank_of += cand.key[j] > q;
+        const ulonglong2* two = reinterpret_cast<const ulonglong2*>(cand.key);
+#pragma unroll 4
+        for (int j = 0; j < n / 2; ++j) {
+          const ulonglong2 o = two[j];
+          rank_of += (o.x > q) + (o.y > q);
+        }
+        if (n & 1) rank_of += cand.key[n - 1] > q;
         if (rank_of < a.top_k) out(rank_of, q);
       }
       for (int i = n + tid; i < a.top_k; i += kThreads) out(i, 0);   // slots nothing fills
@@ -360,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 4 : 5)
 constexpr int kBwdUnits = 4;
 
 template <typename IT, typename GT>
-__global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobsBwdArgs a, int blocks) {
+__global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const LogprobsBwdArgs a, int blocks) {
   constexpr int kN = Unit<IT>::kN;
   const int64_t t = blockIdx.x / static_cast<unsigned>(blocks);
   const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks));
@@ -377,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobsBw
   uint4 w[kBwdUnits];
 #pragma unroll
   for (int i = 0; i < kBwdUnits; ++i) {
-    const int u = u0 + i * kThreads + tid;
+    const int u = u0 + i * kBwdThreads + tid;
     w[i] = !zero && u < u1 ? ld_unit(row + shape.head + static_cast<int64_t>(u) * kN)
                            : make_uint4(0, 0, 0, 0);
   }
@@ -404,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobsBw
   };
 #pragma unroll
   for (int i = 0; i < kBwdUnits; ++i) {
-    const int u = u0 + i * kThreads + tid;
+    const int u = u0 + i * kBwdThreads + tid;
     if (u >= u1) break;
     const int64_t j0 = shape.head + static_cast<int64_t>(u) * kN;
     const int at = static_cast<int>(min(max(y - j0, static_cast<int64_t>(-1)), static_cast<int64_t>(kN)));
@@ -427,9 +534,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobsBw
 // the partial results meet in a fixed order.  One token per lane and eight
 // slices at a time took 25 us of a T = 500, v = 50304 call, this takes 4.
 constexpr int kCombTokens = 8;
-constexpr int kCombSlices = kThreads / kCombTokens;
+constexpr int kCombSlices = kBwdThreads / kCombTokens;
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kBwdThreads)
     linear_logprobs_combine_kernel(const float* __restrict__ stat_m,
                                    const float* __restrict__ stat_s,
                                    const float* __restrict__ stat_u,
@@ -438,9 +545,9 @@ __global__ void __launch_bounds__(kThreads)
                                    int nslices, float scale, float* __restrict__ logprob,
                                    float* __restrict__ entropy, float* __restrict__ lse,
                                    int32_t* dev_status) {
-  __shared__ float part_m[kWarps][kCombTokens];
-  __shared__ float part_s[kWarps][kCombTokens];
-  __shared__ float part_u[kWarps][kCombTokens];
+  __shared__ float part_m[kBwdWarps][kCombTokens];
+  __shared__ float part_s[kBwdWarps][kCombTokens];
+  __shared__ float part_u[kBwdWarps][kCombTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tok = lane & (kCombTokens - 1);
   const int first = threadIdx.x / kCombTokens;
@@ -457,7 +564,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   float M = part_m[0][tok];
 #pragma unroll
-  for (int q = 1; q < kWarps; ++q) M = fmaxf(M, part_m[q][tok]);
+  for (int q = 1; q < kBwdWarps; ++q) M = fmaxf(M, part_m[q][tok]);
   if (M == -CUDART_INF_F) M = 0.0f;   // nothing but −inf (or NaN) in the row
   float S = 0.0f, U = 0.0f;
   if (ok) {
@@ -484,7 +591,7 @@ __global__ void __launch_bounds__(kThreads)
     S = 0.0f;
     U = 0.0f;
 #pragma unroll
-    for (int q = 0; q < kWarps; ++q) {
+    for (int q = 0; q < kBwdWarps; ++q) {
       S += part_s[q][tok];
       U += part_u[q][tok];
     }
@@ -509,15 +616,29 @@ namespace {
 
 template <typename IT, bool kTop>
 tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
-  // Blocks per row: one once the rows alone fill the GPU's resident blocks,
-  // else up to eight (the portable cluster size) while each keeps a step or
-  // more of the row.
+  // Blocks per row: one once the rows alone fill the GPU, else up to eight
+  // (the portable cluster size) while each keeps a step or more of the row.
+  // v = 50304, fp32: 128 rows on 1, 4, 8 blocks each take 13.9, 6.8, 8.0 us, 512
+  // rows on 1, 2, 4 take 32.7, 21.4, 24.8; with 20 alternatives, whose joining
+  // costs more, 16.7, 13.0, 15.6 and 29.4, 25.3, 34.7.
   const int64_t units = a.v / Unit<IT>::kN;
+  const int64_t most = (kTop ? 4 : 7) * num_sms();
   int slices = 1;
-  while (slices < 8 && a.T * slices * 2 <= 4 * num_sms() && units / (slices * 2) >= 2 * kThreads)
+  while (slices < 8 && a.T * slices * 2 <= most && units / (slices * 2) >= 2 * kThreads)
     slices *= 2;
-  constexpr size_t smem = kTop ? sizeof(Candidates<kThreads * Unit<IT>::kN>) : 0;
-  static_assert(smem <= 48 * 1024, "within the default limit of dynamic shared memory");
+  size_t smem = 0;
+  if constexpr (kTop) {
+    using Cand = Candidates;
+    const int64_t per = (units + slices - 1) / slices;
+    const int64_t steps = (per + step_units(true) * kThreads - 1) / (step_units(true) * kThreads);
+    int log = 0;
+    while ((static_cast<int64_t>(Cand::kGroups) << log) < steps) ++log;
+    const int64_t groups = (steps + (1 << log) - 1) >> log;
+    smem = sizeof(Cand) + (groups + 3) / 4 * kThreads * sizeof(float4);
+    static_assert(Cand::kGroups <= 32 && sizeof(Cand) + Cand::kGroups * kThreads * sizeof(float) <= 48 * 1024,
+                  "within the default limit of dynamic shared memory");
+    static_assert(Cand::kRoom >= 8 * kLogprobsMaxK, "room for the slices' best");
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T * slices));
   cfg.blockDim = dim3(kThreads);
@@ -541,9 +662,9 @@ tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
 template <typename IT, typename GT>
 tp_status logprobs_bwd_launch_t(const LogprobsBwdArgs& a, cudaStream_t stream) {
   const int64_t units = a.v / Unit<IT>::kN;
-  const int64_t blocks = units > 0 ? (units + kThreads * kBwdUnits - 1) / (kThreads * kBwdUnits) : 1;
+  const int64_t blocks = units > 0 ? (units + kBwdThreads * kBwdUnits - 1) / (kBwdThreads * kBwdUnits) : 1;
   if (a.T * blocks > 0x7fffffff) return TP_ERR_UNSUPPORTED;   // more logits than any GPU holds
-  logprobs_bwd_kernel<IT, GT><<<static_cast<unsigned>(a.T * blocks), kThreads, 0, stream>>>(
+  logprobs_bwd_kernel<IT, GT><<<static_cast<unsigned>(a.T * blocks), kBwdThreads, 0, stream>>>(
       a, static_cast<int>(blocks));
   note_launches(1);
   return last_error();
@@ -575,7 +696,7 @@ tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_
                                          int32_t* dev_status, cudaStream_t stream) {
   const int nslices = static_cast<int>((v + kXentSlice - 1) / kXentSlice);
   linear_logprobs_combine_kernel<<<static_cast<unsigned>((T + kCombTokens - 1) / kCombTokens),
-                                   kThreads, 0, stream>>>(stat_m, stat_s, stat_u, tgt_logit, targets, T, v,
+                                   kBwdThreads, 0, stream>>>(stat_m, stat_s, stat_u, tgt_logit, targets, T, v,
                                              nslices, scale, logprob, entropy, lse, dev_status);
   note_launches(1);
   return last_error();
