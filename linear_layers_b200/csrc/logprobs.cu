@@ -461,9 +461,12 @@ __global__ void __launch_bounds__(kThreads, kTop ? (Unit<IT>::kN == 4 ? 8 : 7) :
     });
 }
 
-// Gradient of (log-probability, entropy): one pass over the logits, each
-// block a contiguous range of one row, every thread's loads of its (up to)
-// four units in flight at once.
+// Gradient of (log-probability, entropy), with lp = scale·x − lse and p = exp(lp):
+//   scale·(g·[j = y] − p·(g + e·(lp + h))) = p·(e'·lp + c) + [j = y]·scale·g,
+//   e' = −scale·e,  c = −scale·(g + e·h)
+// One pass over the logits, bound by their bytes and the gradient's: each block
+// a contiguous range of one row, every thread's loads of its (up to) four
+// units in flight at once.  8192 rows of 50304, fp32 to bf16: 390 us, 6.3 TB/s.
 constexpr int kBwdUnits = 4;
 
 template <typename IT, typename GT>
@@ -478,53 +481,71 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
   const int per = (shape.units + blocks - 1) / blocks;
   const int u0 = min(part * per, shape.units), u1 = min(u0 + per, shape.units);
   const int tid = threadIdx.x;
+  // this thread's edge element, if any
+  int edge = -1;
+  if (part == 0 && tid < shape.head) edge = tid;
+  if (part == blocks - 1 && tid >= 32 && tid < 32 + shape.tail)
+    edge = shape.head + shape.units * kN + tid - 32;
   const float g = a.dlogprob ? a.dlogprob[t] : 0.0f;
   const float e = a.dentropy ? a.dentropy[t] : 0.0f;
-  const bool zero = g == 0.0f && e == 0.0f;   // a padded row: nothing of it is read
+  if (g == 0.0f && e == 0.0f) {   // a padded row: nothing of it is read
+    const float z[kN] = {};
+    for (int u = u0 + tid; u < u1; u += kBwdThreads)
+      put_unit<kN>(out + shape.head + static_cast<int64_t>(u) * kN, z);
+    if (edge >= 0) put(out + edge, 0.0f);
+    return;
+  }
   uint4 w[kBwdUnits];
 #pragma unroll
   for (int i = 0; i < kBwdUnits; ++i) {
     const int u = u0 + i * kBwdThreads + tid;
-    w[i] = !zero && u < u1 ? ld_unit(row + shape.head + static_cast<int64_t>(u) * kN)
-                           : make_uint4(0, 0, 0, 0);
+    w[i] = u < u1 ? ld_unit(row + shape.head + static_cast<int64_t>(u) * kN) : make_uint4(0, 0, 0, 0);
   }
+  const float edge_x = edge >= 0 ? to_f32(row[edge]) : 0.0f;
   int64_t y = -1;
-  float bad = 0.0f, lse = 0.0f, h = 0.0f;
-  if (!zero) {
-    if (g != 0.0f) {
-      y = a.targets[t];
-      if (y < 0 || y >= a.v) {
-        bad = CUDART_NAN_F;
-        if (part == 0 && tid == 0 && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
-      }
+  float c = -a.scale * g;
+  const float e1 = -a.scale * e;
+  if (g != 0.0f) {
+    y = a.targets[t];
+    if (y < 0 || y >= a.v) {
+      c = CUDART_NAN_F;   // the whole row
+      if (part == 0 && tid == 0 && a.dev_status) atomicOr(a.dev_status, TP_DEVERR_RANGE);
     }
-    lse = a.lse[t];
-    if (e != 0.0f) h = a.entropy[t];
   }
-  const float geh = fmaf(e, h, g);
-  // scale·(g·[j = y] − p·(g + e·(lp + h))), lp = scale·x − lse, p = exp(lp)
-  auto grad = [&](float x, bool at_y) {
-    const float lp = fmaf(x, a.scale, -lse);
-    const float p = ex2_approx(lp * kLog2e);
-    const float d = (at_y ? g : 0.0f) - p * fmaf(e, max_nan(lp, kLowest), geh);
-    return zero ? 0.0f : fmaf(a.scale, d, bad);
+  if (e != 0.0f) c = fmaf(e1, a.entropy[t], c);
+  const float nlse = -a.lse[t];
+  const float2 sc2 = make_float2(a.scale, a.scale), nl2 = make_float2(nlse, nlse);
+  const float2 l2e2 = make_float2(kLog2e, kLog2e);
+  const float2 e2 = make_float2(e1, e1), c2 = make_float2(c, c);
+  auto grad2 = [&](float x0, float x1) {
+    float2 lp = __ffma2_rn(make_float2(x0, x1), sc2, nl2);
+    const float2 q = __fmul2_rn(lp, l2e2);
+    const float2 p = make_float2(ex2_approx(q.x), ex2_approx(q.y));
+    lp = make_float2(max_nan(lp.x, kLowest), max_nan(lp.y, kLowest));
+    return __fmul2_rn(p, __ffma2_rn(e2, lp, c2));
   };
+  const float at_y = a.scale * g;
 #pragma unroll
   for (int i = 0; i < kBwdUnits; ++i) {
     const int u = u0 + i * kBwdThreads + tid;
     if (u >= u1) break;
     const int64_t j0 = shape.head + static_cast<int64_t>(u) * kN;
-    const int at = static_cast<int>(min(max(y - j0, static_cast<int64_t>(-1)), static_cast<int64_t>(kN)));
     float x[kN];
     Unit<IT>::unpack(w[i], x);
 #pragma unroll
-    for (int q = 0; q < kN; ++q) x[q] = grad(x[q], q == at);
+    for (int q = 0; q < kN; q += 2) {
+      const float2 d = grad2(x[q], x[q + 1]);
+      x[q] = d.x;
+      x[q + 1] = d.y;
+    }
+    if (y >= j0 && y < j0 + kN) {
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        if (j0 + q == y) x[q] += at_y;
+    }
     put_unit<kN>(out + j0, x);
   }
-  auto edge = [&](int64_t j) { put(out + j, grad(zero ? 0.0f : to_f32(row[j]), j == y)); };
-  if (part == 0 && tid < shape.head) edge(tid);
-  if (part == blocks - 1 && tid >= 32 && tid < 32 + shape.tail)
-    edge(shape.head + static_cast<int64_t>(shape.units) * kN + tid - 32);
+  if (edge >= 0) put(out + edge, grad2(edge_x, 0.0f).x + (edge == y ? at_y : 0.0f));
 }
 
 // Combine of the per-slice statistics of the output-layer GEMM (slice k of
