@@ -19,7 +19,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 #include <type_traits>
 
 #include "internal.h"
@@ -165,36 +164,36 @@ __global__ void __launch_bounds__(kPrepWarps * 32)
       const uint32_t bit = static_cast<uint32_t>(r.id[i]) & (kSeenWords * 32 - 1);
       again |= ((atomicOr(&seen[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u) << i;
     }
-  if (__any_sync(0xffffffffu, again)) {
-    // a token twice, or two tokens on one bit: looked up, slot group by slot group
+  bool twice = false;   // (the whole warp's answer)
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    // a token twice, or two tokens on one bit: its slots are counted
+    for (uint32_t m = __ballot_sync(0xffffffffu, (again >> i) & 1u); m; m &= m - 1) {
+      const int32_t id = __shfl_sync(0xffffffffu, r.id[i], __ffs(m) - 1);
+      int n = 0;
+#pragma unroll
+      for (int q = 0; q < S; ++q) n += r.id[q] == id;
+      twice |= __reduce_add_sync(0xffffffffu, n) > 1;
+    }
+  if (twice) {
 #pragma unroll
     for (int i = 0; i < S; ++i)
       listed[warp][lane + 32 * i] = make_int2(r.id[i], __float_as_int(r.p[i]));
     __syncwarp();
-    bool twice = false;
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (__any_sync(0xffffffffu, (again >> i) & 1u)) {
+    for (int i = 0; i < S; ++i) {
+      float sum = 0.0f;
+      bool first = true;
 #pragma unroll 8
-        for (int q = 0; q < 32 * S; ++q)
-          twice |= r.id[i] >= 0 && listed[warp][q].x == r.id[i] && q != lane + 32 * i;
-      }
-    if (__any_sync(0xffffffffu, twice)) {
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        float sum = 0.0f;
-        bool first = true;
-#pragma unroll 8
-        for (int q = 0; q < 32 * S; ++q) {   // in slot order
-          const int2 e = listed[warp][q];
-          if (e.x == r.id[i]) {
-            if (q < lane + 32 * i) first = false;
-            sum += __int_as_float(e.y);
-          }
+      for (int q = 0; q < 32 * S; ++q) {   // in slot order
+        const int2 e = listed[warp][q];
+        if (e.x == r.id[i]) {
+          if (q < lane + 32 * i) first = false;
+          sum += __int_as_float(e.y);
         }
-        r.p[i] = sum;
-        if (!first) r.id[i] = -1;
       }
+      r.p[i] = sum;
+      if (!first) r.id[i] = -1;
     }
   }
 #pragma unroll
@@ -704,7 +703,6 @@ tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_
          (units > 22 * 480 * slices ||
           (a.T * slices * 2 <= num_sms() && units * 16 >= 8192 * slices)))
     slices *= 2;
-  if (const char* e = getenv("TPX_SL")) slices = atoi(e);
   const int per = static_cast<int>((units + slices - 1) / slices);
   if (per <= 4 * 128) return launch<IT, GT, 4, 128>(a, slots, slices, per, stream);
   if (per <= 8 * 128) return launch<IT, GT, 8, 128>(a, slots, slices, per, stream);

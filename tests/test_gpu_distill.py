@@ -112,11 +112,45 @@ def test_ragged_weighted_duplicates_and_temperature(renormalize):
     check(x, ids, t, F32, renormalize, w, scale=1.5, with_grad=False)
 
 
-@pytest.mark.parametrize("v,T", [(200001, 3), (300000, 2), (20011, 1), (20011, 900)])
-def test_large_vocabulary_and_many_rows(v, T):
-    x, _ = model_logits(T, v, F32, seed=v)
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("v,T", [(200001, 3), (337920, 2), (20011, 1), (20011, 900)])
+def test_large_vocabulary_and_many_rows(dtype, v, T):
+    x, _ = model_logits(T, v, dtype, seed=v)
     ids, t = entries(T, v, 50, seed=5)
+    check(x, ids, t, dtype)
+
+
+def test_loss_alone_has_no_widest_row():
+    x, _ = model_logits(3, 400003, F32, seed=3)
+    ids, t = entries(3, 400003, 17, seed=6, ragged=True)
+    check(x, ids, t, with_grad=False)
+
+
+@pytest.mark.parametrize("v", [2000, 6600, 9000, 13000, 16700, 20600, 26000, 32003, 42000, 53001, 80000])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_every_width_of_block(dtype, v):
+    """More rows than resident blocks, so that every block turns its buffers
+    over; odd widths, a token three times among the slots, some rows padded."""
+    T = 450 if v < 30000 else 170
+    x, _ = model_logits(T, v, dtype, seed=v)
+    ids, t = entries(T, v, 9, seed=v, duplicates=True)
+    w = torch.ones(T)
+    w[::7] = 0.0
+    check(x, ids, t, dtype, weight=w, grad_scale=1 / T)
+
+
+@pytest.mark.parametrize("K", [31, 32, 33, 64, 65, 128, 129, 256])
+def test_every_number_of_slots(K):
+    """All slots one token, all of them different, and a few repeated far apart."""
+    v, T = 4099, 6
+    x, _ = model_logits(T, v, F32, seed=K)
+    ids, t = entries(T, v, K, seed=K)
+    ids[0] = 17
+    ids[1, K - 1] = ids[1, 0]
+    ids[2, 1::3] = ids[2, 0]
+    ids[3, :] = torch.arange(K) * 2 + 1024 * (torch.arange(K) % 2).to(I32)
     check(x, ids, t, F32)
+    check(x, ids, t, with_grad=False)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])

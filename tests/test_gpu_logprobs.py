@@ -100,6 +100,10 @@ def special_rows(v):
     rows["ascending"] = torch.linspace(-4, 4, v)
     rows["descending"] = torch.linspace(4, -4, v)
     rows["steps"] = (torch.arange(v) // 3).float() * 1e-3
+    rows["many equal at the top"] = torch.where(torch.arange(v) % 3 == 0, 2.0, base.clamp(max=1.0))
+    rows["top in one place"] = base.clamp(max=1.0) + (torch.arange(v) < 400).float() * 9
+    rows["top in one lane"] = base.clamp(max=1.0) + (torch.arange(v) % 2048 < 4).float() * 9
+    rows["equal pairs"] = torch.randn(v, generator=g).mul(8).round()
     rows["sawtooth"] = (torch.arange(v) % 16).float()
     rows["blocks of large"] = (torch.arange(v) % 2048 < 8).float() * 5 + 1e-4 * torch.rand(v, generator=g)
     rows["large offset"] = base + 3000.0
