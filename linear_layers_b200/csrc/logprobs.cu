@@ -153,22 +153,21 @@ struct Candidates {
   }
 };
 
-// Units per thread and step: with alternatives fewer threads are on an SM, and
-// each keeps more bytes in flight.
-constexpr int step_units(bool top) { return top ? 4 : 2; }
+constexpr int kUnits = 4;           // 16-byte units per thread and step
 
 // Log-probability statistics of one row by `slices` blocks (a cluster), each
 // taking a contiguous range of the row's 16-byte units.  A block streams its
 // range with the next step's loads in flight while it adds up the present
 // one; sums and candidates of the blocks meet in block 0 through distributed
-// shared memory.  Reading the row once is the bound for fp32 logits (8192 rows
-// of 50304: 246 us, 6.7 TB/s); bf16 ones take as many instructions for half the
-// bytes (141 us, 5.8 TB/s).
+// shared memory.  Reading the row once is the bound for fp32 logits: 8192 rows
+// of 50304 take 233 us, 7.1 TB/s, with four units a thread and step on eight
+// blocks per SM (two units on ten: 241 us, and 82 against 63 us for 2048 rows,
+// whose last wave has few blocks to keep loads in flight).  bf16 logits take as
+// many instructions for half the bytes: 140 us, 5.9 TB/s.
 template <typename IT, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? (Unit<IT>::kN == 4 ? 8 : 7) : 10)
+__global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
     logprobs_kernel(const LogprobsArgs a, int slices) {
   constexpr int kN = Unit<IT>::kN;
-  constexpr int kUnits = step_units(kTop);
   using Cand = Candidates;
   extern __shared__ __align__(16) uint8_t dyn_smem[];
   Cand& cand = *reinterpret_cast<Cand*>(dyn_smem);   // only touched with kTop
@@ -651,7 +650,7 @@ tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
   if constexpr (kTop) {
     using Cand = Candidates;
     const int64_t per = (units + slices - 1) / slices;
-    const int64_t steps = (per + step_units(true) * kThreads - 1) / (step_units(true) * kThreads);
+    const int64_t steps = (per + kUnits * kThreads - 1) / (kUnits * kThreads);
     int log = 0;
     while ((static_cast<int64_t>(Cand::kGroups) << log) < steps) ++log;
     const int64_t groups = (steps + (1 << log) - 1) >> log;
