@@ -64,6 +64,17 @@ constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 64 + kEpiThreads;
 
+// K in chunks of 1024 (k-blocks per chunk) for the log-probability epilogues,
+// whose warps add the chunks' accumulators up in fp32 registers.  The tensor
+// core's additions into an accumulator truncate: an entropy whose rows' logits
+// have a standard deviation of 4 was off by 5.9e-6 of its size at h = 4096 and by
+// 2.4e-5 at h = 16384 in one chain, by 1.3e-6 and 1.1e-6 with this chunk, by
+// 5e-7 with 512 and 3e-7 with 256.  The price: T = 500, h = 1600, v = 50304 takes 67
+// us in one chain, 70 with chunks of 1024, 82 with 512 and 106 with 256, as a shorter
+// chunk leaves less time for the epilogue that holds the other accumulator.
+constexpr int kChunkKb = 16;
+constexpr bool chunked_k(int epi) { return epi == EPI_LOGP_STATS || epi == EPI_LOGP_GRAD; }
+
 // Epilogues over the rows' softmax (the loss and log-probability statistics
 // and gradients): 256-column tiles, no split.
 constexpr bool softmax_epi(int epi) {
@@ -413,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
   static_assert(RH == 1 || (CG == 2 && BNT == 256), "tall tiles are 2-CTA 256-column tiles");
   static_assert(BNT == 256 || !softmax_epi(EPI),
                 "the softmax epilogues take 128-column slices of a 256-column tile");
+  static_assert(RH == 1 || !chunked_k(EPI), "a chunked tile's sums fill the registers");
   constexpr int STAGES = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       uint32_t phase = 0;
       int t = 0;
       bool ok = true, any = false;
-      for (int unit = slot0; ok && unit < P.total_units; unit += nslots, ++t) {
+      for (int unit = slot0; ok && unit < P.total_units; unit += nslots) {
         const int prob = unit >= P.units0 ? 1 : 0;
         const GemmArgs& a = P.a[prob];
         // one MMA covers 128 rows per CTA (256 for the pair); the tall tile
@@ -574,46 +586,54 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
         const uint32_t b_kstep = a.b_mn ? 2048u : 32u;
         int tm, tn, s, tile;
         unit_map(a, unit - prob * P.units0, tm, tn, s, tile);
-        const int acc = t % C::kAccBufs;
-        const uint32_t use = static_cast<uint32_t>(t / C::kAccBufs);
-        if (!mbar_wait_bounded(&tempty[acc], (use & 1u) ^ 1u, a0.wait_ns, abort_flag)) {
-          if (!*abort_flag) flag_timeout(a0, abort_flag);
-          break;
-        }
-        tc_fence_after_sync();
-        // RH = 1: accumulator buffer acc; RH = 2: row half h at column h·BNT
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BNT);
         const int kb0 = s < 0 ? a.split_kb[0] : a.split_kb[s];
         const int kb1 = s < 0 ? a.split_kb[a.splits] : a.split_kb[s + 1];
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_bounded(&full[stage], phase, a0.wait_ns, abort_flag)) {
+        // one chain of accumulations, or one for each chunk of K
+        int lo = kb0;
+        do {
+          const int hi = chunked_k(EPI) ? min(lo + kChunkKb, kb1) : kb1;
+          const int acc = t % C::kAccBufs;
+          const uint32_t use = static_cast<uint32_t>(t / C::kAccBufs);
+          if (!mbar_wait_bounded(&tempty[acc], (use & 1u) ^ 1u, a0.wait_ns, abort_flag)) {
             if (!*abort_flag) flag_timeout(a0, abort_flag);
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a_base = smem_u32(sA + stage * C::kABytes);
-          const uint32_t b_base = smem_u32(sB + stage * C::kBBytes);
+          // RH = 1: accumulator buffer acc; RH = 2: row half h at column h·BNT
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BNT);
+          for (int kb = lo; kb < hi; ++kb) {
+            if (!mbar_wait_bounded(&full[stage], phase, a0.wait_ns, abort_flag)) {
+              if (!*abort_flag) flag_timeout(a0, abort_flag);
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a_base = smem_u32(sA + stage * C::kABytes);
+            const uint32_t b_base = smem_u32(sB + stage * C::kBBytes);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            const uint64_t bdesc = smem_desc_sw128(b_base + k * b_kstep, b_lbo, 1024);
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t bdesc = smem_desc_sw128(b_base + k * b_kstep, b_lbo, 1024);
 #pragma unroll
-            for (int h = 0; h < RH; ++h) {   // the row halves share the B stage
-              // a row half is 128 rows: 16 KB of the A stage in either layout
-              const uint64_t adesc =
-                  smem_desc_sw128(a_base + h * (BM * 128) + k * a_kstep, a_lbo, 1024);
-              tc_mma_bf16_cg<CG>(d_tmem + static_cast<uint32_t>(h * BNT), adesc, bdesc, idesc,
-                                 (kb > kb0 || k > 0) ? 1u : 0u);
+              for (int h = 0; h < RH; ++h) {   // the row halves share the B stage
+                // a row half is 128 rows: 16 KB of the A stage in either layout
+                const uint64_t adesc =
+                    smem_desc_sw128(a_base + h * (BM * 128) + k * a_kstep, a_lbo, 1024);
+                tc_mma_bf16_cg<CG>(d_tmem + static_cast<uint32_t>(h * BNT), adesc, bdesc, idesc,
+                                   (kb > lo || k > 0) ? 1u : 0u);
+              }
+            }
+            any = true;
+            tc_commit_mc<CG>(&empty[stage], pair_mask);   // frees the stage in both CTAs
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
-          any = true;
-          tc_commit_mc<CG>(&empty[stage], pair_mask);   // frees the stage in both CTAs
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (ok) tc_commit_mc<CG>(&tfull[acc], pair_mask);   // accumulators ready
+          if (ok) tc_commit_mc<CG>(&tfull[acc], pair_mask);   // accumulators ready
+          lo = hi;
+          ++t;
+        } while (ok && lo < kb1);
       }
       if (any) {   // every issued MMA must finish before tensor memory is freed
         volatile int keep_waiting = 0;
@@ -635,6 +655,54 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       const GemmArgs& a = P.a[prob];
       int tm, tn, s, tile;
       unit_map(a, unit - prob * P.units0, tm, tn, s, tile);
+      if constexpr (chunked_k(EPI)) {
+        // add the chunks up and leave the sum in the last one's accumulator
+        const int last = (a.split_kb[1] - a.split_kb[0] - 1) / kChunkKb;
+        bool all = true;
+        float sum[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+#pragma unroll 1
+        for (int ch = 0; last > 0 && ch <= last; ++ch) {
+          const int buf = t % C::kAccBufs;
+          const bool here = mbar_wait_bounded<true>(
+              &tfull[buf], static_cast<uint32_t>(t / C::kAccBufs) & 1u, a0.wait_ns, abort_flag);
+          all = named_barrier_and(1, kEpiThreads, here);
+          if (!all) break;
+          tc_fence_after_sync();
+          const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                              static_cast<uint32_t>(buf * BNT + half * 128);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(at + c * 32, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              sum[c * 32 + j] += __uint_as_float(r[j]);
+              r[j] = __float_as_uint(sum[c * 32 + j]);
+            }
+            if (ch == last) tmem_st_32x32b_x32(at + c * 32, r);
+          }
+          if (ch == last) {
+            tc_wait_st();
+            break;
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2)
+              mbar_arrive_cluster(tempty_addr0 + static_cast<uint32_t>(buf * 8));
+            else
+              mbar_arrive(&tempty[buf]);
+          }
+          ++t;
+        }
+        if (!all) {
+          if (et == 0 && !*abort_flag) flag_timeout(a0, abort_flag);
+          break;
+        }
+      }
       const int acc = t % C::kAccBufs;
       const uint32_t use = static_cast<uint32_t>(t / C::kAccBufs);
       const bool got = mbar_wait_bounded<true>(&tfull[acc], use & 1u, a0.wait_ns, abort_flag);
@@ -1249,10 +1317,12 @@ tp_status launch_epi(const GemmParams& prm, int epi, int slots, cudaStream_t str
       if constexpr (BNT == 256) return launch_impl<CG, BNT, RH, EPI_XENT_GRAD>(prm, slots, stream);
       break;
     case EPI_LOGP_STATS:
-      if constexpr (BNT == 256) return launch_impl<CG, BNT, RH, EPI_LOGP_STATS>(prm, slots, stream);
+      if constexpr (BNT == 256 && RH == 1)
+        return launch_impl<CG, BNT, RH, EPI_LOGP_STATS>(prm, slots, stream);
       break;
     case EPI_LOGP_GRAD:
-      if constexpr (BNT == 256) return launch_impl<CG, BNT, RH, EPI_LOGP_GRAD>(prm, slots, stream);
+      if constexpr (BNT == 256 && RH == 1)
+        return launch_impl<CG, BNT, RH, EPI_LOGP_GRAD>(prm, slots, stream);
       break;
   }
   return TP_ERR_UNSUPPORTED;
@@ -1310,7 +1380,7 @@ TileChoice choose_tile(int M, int N, int K, int splits, int epi) {
     else if (!std::strcmp(e, "2x128")) t = {2, 128, 1};
     else if (!std::strcmp(e, "1x256")) t = {1, 256, 1};
     else if (!std::strcmp(e, "1x128")) t = {1, 128, 1};
-    if (t.cg && !(xent && t.bn != 256)) return t;
+    if (t.cg && !(xent && t.bn != 256) && !(chunked_k(epi) && t.rh == 2)) return t;
   }
   // The tall tile is not among the automatic choices: in the whole layer
   // step (after the logits and the cross-entropy have filled L2 with their

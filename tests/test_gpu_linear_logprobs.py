@@ -2,7 +2,8 @@
 on the GPU against the fp64 oracle.
 
 The GEMM adds h products in fp32, at most h/16 roundings of partial sums of
-size ~10 or less: below 1e-3 of a logit for h <= 4096, and the log-probability
+size ~10 or less: below 1e-3 of a logit for h <= 4096 (in chunks of 1024, whose
+sums are added in fp32, less), and the log-probability
 and entropy follow the logits one to one, so the bar is TOL_XENT relative to
 values of 8 or more, as for the cross-entropy without the logits.  The bf16
 gradient has the bf16 bar.
@@ -35,7 +36,7 @@ def _check_fwd(r, ref):
 
 
 SHAPES = [(1, 2048, 64, 8), (300, 1000, 256, 4), (16, 2048, 64, 8), (200, 136, 512, 2),
-          (513, 4096, 328, 1), (3, 50304, 1600, 4), (130, 8, 8, 1)]
+          (513, 4096, 328, 1), (3, 50304, 1600, 4), (130, 8, 8, 1), (513, 20000, 2056, 1)]
 
 
 @pytest.mark.parametrize("T,v,h,N", SHAPES)
@@ -69,6 +70,38 @@ def test_forward_and_gradient(T, v, h, N, scale):
         if T > 2:
             assert not out[1].any()
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("h", [1024, 1032, 2056, 3080])
+@pytest.mark.parametrize("T,v", [(5, 1000), (300, 2056)])
+def test_hidden_sizes_around_the_accumulation_chunk(T, v, h):
+    H, E, y = _inputs(T, v, h, seed=h)
+    Hd, Ed, yd = H.cuda(), E.cuda(), y.cuda()
+    r = tpl.tp_linear_logprobs_fwd(Hd, Ed, yd, 1)
+    L = O.logits(H, E)
+    _check_fwd(r, O.logprobs(L, y))
+    g = torch.linspace(-1.0, 1.0, T)
+    d = tpl.tp_linear_logprobs_dlogits(Hd, Ed, yd, r["lse"], r["entropy"], g.cuda(), g.cuda(), 1)
+    assert_close("dlogits", d, O.logprobs_bwd(L, y, g, g), TOL_BF16)
+
+
+def test_long_sums_of_one_sign():
+    """Logits of 16 as 65536 positive products.  Within a chunk of 1024 the
+    tensor core adds 64 times and truncates by at most 2^-22 of the sum so far;
+    64 chunk sums are added in fp32 (2^-24 of the sum each); lse adds a few
+    roundings of its 21.  One chain of 4096 truncations would be off by about
+    4096·(1/2)·2^-24.5 = 8.6e-5 of the logits, 1.4e-3."""
+    T, v, h = 16, 136, 65536
+    gen = torch.Generator().manual_seed(3)
+    H = (0.5 + torch.rand(T, h, generator=gen)).bfloat16()
+    E = ((0.5 + torch.rand(v, h, generator=gen)) * (16.0 / h)).bfloat16()
+    y = torch.randint(0, v, (T,), generator=gen)
+    r = tpl.tp_linear_logprobs_fwd(H.cuda(), E.cuda(), y.cuda(), 1)
+    z = H.double().numpy() @ E.double().numpy().T
+    ref = O.logprobs(z, y)
+    tol = z.max() * (64 * 2.0**-22 + 64 * 2.0**-24) + 8 * 21 * 2.0**-24
+    assert np.all(np.abs(f64(r["lse"]) - ref["lse"]) <= tol)
+    assert np.all(np.abs(f64(r["logprob"]) - ref["logprob"]) <= 2 * tol)
 
 
 def test_forward_of_an_odd_vocabulary_without_targets():
