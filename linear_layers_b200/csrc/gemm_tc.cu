@@ -69,9 +69,11 @@ constexpr int kThreads = 64 + kEpiThreads;
 // core's additions into an accumulator truncate: an entropy whose rows' logits
 // have a standard deviation of 4 was off by 5.9e-6 of its size at h = 4096 and by
 // 2.4e-5 at h = 16384 in one chain, by 1.3e-6 and 1.1e-6 with this chunk, by
-// 5e-7 with 512 and 3e-7 with 256.  The price: T = 500, h = 1600, v = 50304 takes 67
-// us in one chain, 70 with chunks of 1024, 82 with 512 and 106 with 256, as a shorter
-// chunk leaves less time for the epilogue that holds the other accumulator.
+// 5e-7 with 512 and 3e-7 with 256.  The price, T = 500, h = 1600, v = 50304: 68.4
+// us in one chain, 69.7 with chunks of 1024, 80 with 512 and 107 with 256 (about
+// 1 us a readout of a tile's 12.8).  The epilogue works on the registers, so the
+// last accumulator is free as early as the others: held until the row's stores
+// are done, the gradient of T = 1024, h = 4096 cost 15 % more.
 constexpr int kChunkKb = 16;
 constexpr bool chunked_k(int epi) { return epi == EPI_LOGP_STATS || epi == EPI_LOGP_GRAD; }
 
@@ -650,20 +652,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
     const int et = threadIdx.x - 64;      // 0..255 among the epilogue threads
     const uint32_t tempty_addr0 = CG == 2 ? mapa_shared(&tempty[0], 0) : smem_u32(&tempty[0]);
     int t = 0;
+    // chunked K: the row's sums over the warp's 128 columns
+    [[maybe_unused]] float sum[chunked_k(EPI) ? 128 : 1];
     for (int unit = slot0; unit < P.total_units; unit += nslots, ++t) {
       const int prob = unit >= P.units0 ? 1 : 0;
       const GemmArgs& a = P.a[prob];
       int tm, tn, s, tile;
       unit_map(a, unit - prob * P.units0, tm, tn, s, tile);
       if constexpr (chunked_k(EPI)) {
-        // add the chunks up and leave the sum in the last one's accumulator
-        const int last = (a.split_kb[1] - a.split_kb[0] - 1) / kChunkKb;
+        const int chunks = (a.split_kb[1] - a.split_kb[0] + kChunkKb - 1) / kChunkKb;
         bool all = true;
-        float sum[128];
 #pragma unroll
         for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
 #pragma unroll 1
-        for (int ch = 0; last > 0 && ch <= last; ++ch) {
+        for (int ch = 0;;) {
           const int buf = t % C::kAccBufs;
           const bool here = mbar_wait_bounded<true>(
               &tfull[buf], static_cast<uint32_t>(t / C::kAccBufs) & 1u, a0.wait_ns, abort_flag);
@@ -678,24 +680,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
             tmem_ld_32x32b_x32(at + c * 32, r);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              sum[c * 32 + j] += __uint_as_float(r[j]);
-              r[j] = __float_as_uint(sum[c * 32 + j]);
-            }
-            if (ch == last) tmem_st_32x32b_x32(at + c * 32, r);
-          }
-          if (ch == last) {
-            tc_wait_st();
-            break;
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
           }
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
+          if (lane == 0) {   // the accumulator is free while its sum is worked on
             if constexpr (CG == 2)
               mbar_arrive_cluster(tempty_addr0 + static_cast<uint32_t>(buf * 8));
             else
               mbar_arrive(&tempty[buf]);
           }
+          if (++ch == chunks) break;
           ++t;
         }
         if (!all) {
@@ -705,7 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       }
       const int acc = t % C::kAccBufs;
       const uint32_t use = static_cast<uint32_t>(t / C::kAccBufs);
-      const bool got = mbar_wait_bounded<true>(&tfull[acc], use & 1u, a0.wait_ns, abort_flag);
+      bool got = true;
+      if constexpr (!chunked_k(EPI))
+        got = mbar_wait_bounded<true>(&tfull[acc], use & 1u, a0.wait_ns, abort_flag);
       // all epilogue threads leave together or go on together, so no warp
       // can be left waiting in a later named barrier
       if (!named_barrier_and(1, kEpiThreads, got)) {
@@ -930,16 +927,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           const int64_t tgt = row_ok && a.targets ? a.targets[row] : -1;
           const float sl = a.logit_scale * kLog2e;
           float m = -INFINITY, ssum = 0.0f, usum = 0.0f;
-#pragma unroll 1
-          for (int c = c0; c < c0 + C::kChunks; ++c) {
-            const int col0 = tn * BNT + c * 32;
-            if (col0 >= a.N) break;        // warp-uniform
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_base + c * 32, r);
-            tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col0 = tn * BNT + (c0 + c) * 32;
+            if (col0 >= a.N) continue;     // warp-uniform
             float v[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            for (int j = 0; j < 32; ++j) v[j] = sum[c * 32 + j];
             if (col0 + 32 > a.N) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -1006,17 +1000,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
         const bool zero = g == 0.0f && e == 0.0f;
         const float ls = a.logit_scale;
         const float geh = fmaf(e, ent, g);       // g + e·entropy
-#pragma unroll 1
-        for (int c = c0; c < c0 + C::kChunks; ++c) {
-          const int col0 = tn * BNT + c * 32;
-          if (col0 >= a.N) break;          // warp-uniform
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(t_base + c * 32, r);
-          tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col0 = tn * BNT + (c0 + c) * 32;
+          if (col0 >= a.N) continue;       // warp-uniform
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float lp = fmaf(__uint_as_float(r[j]), ls, -lse);
+            const float lp = fmaf(sum[c * 32 + j], ls, -lse);
             const float p = ex2_approx(lp * kLog2e);
             const float d = (col0 + j == tgt ? g : 0.0f) - p * fmaf(e, fmaxf(lp, -1e30f), geh);
             v[j] = zero ? 0.0f : fmaf(ls, d, bad);
@@ -1145,7 +1136,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       }   // row halves
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) {   // release the accumulator to the pair leader's MMA
+      if (!chunked_k(EPI) && lane == 0) {   // release the accumulator to the pair leader's MMA
         if constexpr (CG == 2)
           mbar_arrive_cluster(tempty_addr0 + static_cast<uint32_t>(acc * 8));
         else
