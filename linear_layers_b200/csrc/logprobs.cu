@@ -75,9 +75,10 @@ __device__ __forceinline__ uint64_t warp_rth_key(uint64_t key, uint64_t second, 
 // the range is read once more in barrier-separated steps, and whenever kLimit
 // candidates have gathered the threshold is raised among them and the rest
 // dropped.
-// 8192 bf16 rows of 50304 take 141 us without alternatives, 190 at k = 1, 241 at
-// k = 64, 319 at k = 128: the instructions behind a row's last load.  Gathering while streaming, against a threshold from the first
-// elements, took twice the instructions.
+// 8192 bf16 rows of 50304 take 141 us without alternatives, 185 at k = 1, 237 at
+// k = 64, 314 at k = 128: the instructions behind a row's last load.  Gathering
+// while streaming, against a threshold from the first elements, took twice the
+// instructions.
 struct Candidates {
   static constexpr int kLimit = 512;
   static constexpr int kRoom = kLimit + kThreads * 8 + 16;   // kLimit and a step of units
@@ -465,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
 //   e' = −scale·e,  c = −scale·(g + e·h)
 // One pass over the logits, bound by their bytes and the gradient's: each block
 // a contiguous range of one row, every thread's loads of its (up to) four
-// units in flight at once.  8192 rows of 50304, fp32 to bf16: 390 us, 6.3 TB/s.
+// units in flight at once.  8192 rows of 50304, fp32 to bf16, one row in eight
+// padded (written as zeros, not read): 335 us, 6.8 TB/s; on single elements
+// instead of packed pairs the same took 396 us.
 constexpr int kBwdUnits = 4;
 
 template <typename IT, typename GT>
