@@ -9,6 +9,7 @@ values of 8 or more, as for the cross-entropy without the logits.  The bf16
 gradient has the bf16 bar.
 """
 import math
+import time
 
 import numpy as np
 import pytest
@@ -176,3 +177,38 @@ def test_workspace_is_shared_by_two_captured_graphs_in_turn():
     for _, r in graphs:
         for k in want:
             assert torch.equal(r[k], want[k]), k
+
+
+@pytest.mark.parametrize("tile", ["2x256", "1x256", "2x256t", "1x128"])
+@pytest.mark.parametrize("unit,kblock", [(0, 1), (0, 20), (1, 16), (1, 33)])
+def test_a_stalled_producer_times_out_and_the_next_call_is_right(tile, unit, kblock, monkeypatch):
+    """The GEMM's bounded waits between the chunks of K (36 k-blocks of 64, 16 to a
+    chunk) end by their limit and leave the context usable.  The tile shapes
+    that these epilogues do not take fall back to one that they do."""
+    monkeypatch.setenv("TP_GEMM_TILE", tile)
+    T, v, h = 300, 1024, 2304
+    H, E, y = _inputs(T, v, h, seed=9)
+    Hd, Ed, yd = H.cuda(), E.cuda(), y.cuda()
+    L = O.logits(H, E)
+    ref = O.logprobs(L, y)
+    g = torch.ones(T)
+    lse = torch.from_numpy(ref["lse"]).float().cuda()
+    gd = g.cuda()
+    torch.cuda.synchronize()
+    for call in (lambda st: tpl.tp_linear_logprobs_fwd(Hd, Ed, yd, 1, dev_status=st),
+                 lambda st: tpl.tp_linear_logprobs_dlogits(Hd, Ed, yd, lse, None, gd, None, 1,
+                                                           dev_status=st)):
+        st = tpl.new_status()
+        tpl.tp_debug_stall_next_gemm(unit, kblock, wait_limit_us=50000)
+        t0 = time.perf_counter()
+        call(st)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 2.0
+        assert int(st.item()) & tpl.DEVERR_TIMEOUT
+        st = tpl.new_status()
+        out = call(st)
+        assert int(st.item()) == 0
+        if isinstance(out, dict):
+            _check_fwd(out, ref)
+        else:
+            assert_close("dlogits", out, O.logprobs_bwd(L, y, g, None), TOL_BF16)
