@@ -206,20 +206,25 @@ __global__ void __launch_bounds__(kPrepWarps * 32)
 
 // Without a gradient the logits are needed once: the rows' sums come from the
 // log-probability kernel (sums [T] of (r, log S)), and one warp per row gathers
-// the listed logits.
+// the listed logits, beside that kernel's last rows.
 template <typename IT, int S>
 __global__ void __launch_bounds__(kPrepWarps * 32)
     distill_loss_kernel(const DistillArgs a, const float2* __restrict__ sums) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepWarps + (threadIdx.x >> 5);
+  grid_dependents_launch();
   if (t >= a.T) return;
   const RowSlots<S> r(a, t, lane);
+  float x[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    x[i] = r.id[i] >= 0 ? to_f32(static_cast<const IT*>(a.logits)[t * a.v + r.id[i]]) : 0.0f;
+  grid_dependency_wait();   // nothing above is written by the kernel before
   const float2 rs = sums[t];
   float A = 0.0f;
 #pragma unroll
   for (int i = 0; i < S; ++i)
-    if (r.id[i] >= 0)
-      A = fmaf(r.p[i], to_f32(static_cast<const IT*>(a.logits)[t * a.v + r.id[i]]) - rs.x, A);
+    if (r.id[i] >= 0) A = fmaf(r.p[i], x[i] - rs.x, A);
   A = warp_sum(A);
   if (lane == 0) {
     const float w = a.weight ? a.weight[t] : 1.0f;
@@ -749,15 +754,29 @@ tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, fl
     l.lse = a.lse;
     l.sums = static_cast<float2*>(ws);
     if (tp_status st = logprobs_fwd_launch(l, dt, stream)) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(prep);
+    cfg.blockDim = dim3(kPrepWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t err = cudaSuccess;
     with_slots(a.K, [&](auto s) {
-      if (dt == TP_DTYPE_BF16)
-        distill_loss_kernel<__nv_bfloat16, s()><<<prep, kPrepWarps * 32, 0, stream>>>(a, l.sums);
-      else
-        distill_loss_kernel<float, s()><<<prep, kPrepWarps * 32, 0, stream>>>(a, l.sums);
+      err = dt == TP_DTYPE_BF16
+                ? cudaLaunchKernelEx(&cfg, distill_loss_kernel<__nv_bfloat16, s()>, a,
+                                     static_cast<const float2*>(l.sums))
+                : cudaLaunchKernelEx(&cfg, distill_loss_kernel<float, s()>, a,
+                                     static_cast<const float2*>(l.sums));
     });
+    if (err != cudaSuccess) {
+      cudaGetLastError();
+      return TP_ERR_CUDA;
+    }
     note_launches(1);
-    if (cudaGetLastError() != cudaSuccess) return TP_ERR_CUDA;
-    return loss_sum ? loss_sum_launch(a.loss, a.T, loss_sum, stream) : TP_OK;
+    return loss_sum ? loss_sum_launch(a.loss, a.T, loss_sum, stream, true) : TP_OK;
   }
   float4* info = static_cast<float4*>(ws);
   int2* entries = reinterpret_cast<int2*>(info + a.T);

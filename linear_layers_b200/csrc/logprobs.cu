@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
   const int tid = threadIdx.x;
   const float sl = a.scale * kLog2e;
   const float tau = 8.0f / sl;
+  if (a.sums) grid_dependents_launch();   // the distillation loss follows
 
   // the given token's logit, in flight behind the row
   int64_t y = -1;
