@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32)
 // the listed logits, beside that kernel's last rows.
 template <typename IT, int S>
 __global__ void __launch_bounds__(kPrepWarps * 32)
-    distill_loss_kernel(const DistillArgs a, const float2* __restrict__ sums) {
+    distill_loss_kernel(const DistillArgs a, const float2* sums) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepWarps + (threadIdx.x >> 5);
   grid_dependents_launch();
