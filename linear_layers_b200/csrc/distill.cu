@@ -699,15 +699,23 @@ template <typename IT, typename GT>
 tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_t stream) {
   constexpr int kN = Unit<IT>::kN;
   const int64_t units = (a.v + kN - 1) / kN;
-  // Slices of a row: as few as hold it.  A row of 50304 fp32 logits in
-  // gradient steps of 8192 rows took 411 us on two blocks of 512 threads, 643 us
-  // on eight of 128: every exchange waits for the last of the row's blocks.
+  // Slices of a row: as few of 1, 2, 4, 6 and 8 as hold it.  A row of 50304 fp32
+  // logits in gradient steps of 8192 rows took 411 us on two blocks of 512
+  // threads, 643 us on eight of 128: every exchange waits for the last of the
+  // row's blocks.  Clusters have to fit the GPU's processing clusters: 22 of six
+  // blocks are resident, 15 of eight, 26 of five and 45 of three, and 500 fp32
+  // rows of 200001 took 137, 161 and 165 us on six, eight and five, 800 rows of
+  // 100000 117 and 121 us on four and three.
   // With few rows, more slices while each keeps 4 KB.
   int slices = 1;
-  while (slices < kMaxSlices &&
-         (units > 22 * 480 * slices ||
-          (a.T * slices * 2 <= num_sms() && units * 16 >= 8192 * slices)))
-    slices *= 2;
+  for (;;) {
+    const int next = slices < 4 ? 2 * slices : slices + 2;
+    if (next > kMaxSlices) break;
+    if (units <= 22 * 480 * slices &&
+        !(a.T * next <= num_sms() && units * 16 >= 4096 * static_cast<int64_t>(next)))
+      break;
+    slices = next;
+  }
   const int per = static_cast<int>((units + slices - 1) / slices);
   if (per <= 4 * 128) return launch<IT, GT, 4, 128>(a, slots, slices, per, stream);
   if (per <= 8 * 128) return launch<IT, GT, 8, 128>(a, slots, slices, per, stream);
@@ -717,7 +725,7 @@ tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_
   if (per <= 8 * 512) return launch<IT, GT, 8, 512>(a, slots, slices, per, stream);
   if (per <= 10 * 512) return launch<IT, GT, 10, 512>(a, slots, slices, per, stream);
   if (per <= 13 * 512) return launch<IT, GT, 13, 512>(a, slots, slices, per, stream);
-  if (per <= 16 * 512) return launch<IT, GT, 16, 512>(a, slots, slices, per, stream);
+  if (per <= 18 * 480) return launch<IT, GT, 18, 480>(a, slots, slices, per, stream);
   if (per <= 22 * 480) return launch<IT, GT, 22, 480>(a, slots, slices, per, stream);
   return TP_ERR_UNSUPPORTED;
 }

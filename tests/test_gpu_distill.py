@@ -139,6 +139,17 @@ def test_every_width_of_block(dtype, v):
     check(x, ids, t, dtype, weight=w, grad_scale=1 / T)
 
 
+@pytest.mark.parametrize("v,T", [(34003, 320), (66007, 160), (140001, 80), (200003, 60), (260003, 40),
+                                 (50257, 20), (8203, 23), (8203, 13)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_every_number_of_blocks_to_a_row(dtype, v, T):
+    """One to eight blocks (six and eight for the widest fp32 rows, and for few
+    rows of any width), several rows to a block."""
+    x, _ = model_logits(T, v, dtype, seed=v + T)
+    ids, t = entries(T, v, 20, seed=v, duplicates=True)
+    check(x, ids, t, dtype, grad_scale=1.0 / T)
+
+
 @pytest.mark.parametrize("K", [31, 32, 33, 64, 65, 128, 129, 256])
 def test_every_number_of_slots(K):
     """All slots one token, all of them different, and a few repeated far apart."""
