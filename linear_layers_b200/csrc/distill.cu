@@ -33,7 +33,7 @@ constexpr int kMaxSlices = 8;
 // Blocks of NT streaming threads with R units each that the registers of an
 // SM are shared by.
 constexpr int blocks_per_sm(int R, int NT) {
-  return NT == 128 ? (R <= 4 ? 8 : 4) : NT == 256 || R <= 8 ? 2 : 1;
+  return NT == 128 ? (R <= 4 ? 8 : 4) : NT == 256 || R <= 9 ? 2 : 1;
 }
 // 1-D bulk copy global -> this CTA's shared memory, completion counted in
 // bytes on `bar` (16-byte aligned addresses, size a multiple of 16).
@@ -722,7 +722,7 @@ tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_
   if (per <= 13 * 128) return launch<IT, GT, 13, 128>(a, slots, slices, per, stream);
   if (per <= 10 * 256) return launch<IT, GT, 10, 256>(a, slots, slices, per, stream);
   if (per <= 13 * 256) return launch<IT, GT, 13, 256>(a, slots, slices, per, stream);
-  if (per <= 8 * 512) return launch<IT, GT, 8, 512>(a, slots, slices, per, stream);
+  if (per <= 9 * 480) return launch<IT, GT, 9, 480>(a, slots, slices, per, stream);
   if (per <= 10 * 512) return launch<IT, GT, 10, 512>(a, slots, slices, per, stream);
   if (per <= 13 * 512) return launch<IT, GT, 13, 512>(a, slots, slices, per, stream);
   if (per <= 18 * 480) return launch<IT, GT, 18, 480>(a, slots, slices, per, stream);
