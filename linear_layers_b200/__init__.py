@@ -707,6 +707,13 @@ def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, ent
     dev = logits.device
     if targets is None and logprob is not None:
         raise ValueError("logprob needs targets")
+    if top_k <= 0 and (top_idx is not None or top_logprob is not None):
+        raise ValueError("top_idx and top_logprob need top_k > 0")
+    _contig(logits, targets, logprob, entropy, lse, top_idx, top_logprob)
+    _want(dev, ("targets", targets, (T,), _I64T), ("logprob", logprob, (T,), _F32),
+          ("entropy", entropy, (T,), _F32), ("lse", lse, (T,), _F32),
+          ("top_idx", top_idx, (T, top_k), _I32T), ("top_logprob", top_logprob, (T, top_k), _F32),
+          _status_spec(dev_status))
     if targets is None:
         entropy, lse = _row_outputs(T, dev, entropy, lse)
     else:
@@ -716,13 +723,6 @@ def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, ent
             top_idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
         if top_logprob is None:
             top_logprob = torch.empty(T, top_k, dtype=torch.float32, device=dev)
-    elif top_idx is not None or top_logprob is not None:
-        raise ValueError("top_idx and top_logprob need top_k > 0")
-    _contig(logits, targets, logprob, entropy, lse, top_idx, top_logprob)
-    _want(dev, ("targets", targets, (T,), _I64T), ("logprob", logprob, (T,), _F32),
-          ("entropy", entropy, (T,), _F32), ("lse", lse, (T,), _F32),
-          ("top_idx", top_idx, (T, top_k), _I32T), ("top_logprob", top_logprob, (T, top_k), _F32),
-          _status_spec(dev_status))
     _check(_launch(lib().vp_logprobs_fwd, dev, _ptr(logits), _dt(logits), _ptr(targets), T, v,
                    N, float(scale), int(top_k), _ptr(logprob), _ptr(entropy), _ptr(lse),
                    _ptr(top_idx), _ptr(top_logprob), _ptr(dev_status)), "vp_logprobs_fwd")
@@ -788,15 +788,15 @@ def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weig
     T, v = logits.shape
     dev = logits.device
     K = teacher_ids.shape[1]
-    loss, lse = _row_outputs(T, dev, loss, lse)
-    loss_sum = torch.empty(1, dtype=torch.float32, device=dev) if loss_sum is None else loss_sum
-    if with_grad and dlogits is None:
-        dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
     _contig(logits, teacher_ids, teacher_logits, weight, loss, loss_sum, lse, dlogits)
     _want(dev, ("teacher_ids", teacher_ids, (T, K), _I32T),
           ("teacher_logits", teacher_logits, (T, K), _F32), ("weight", weight, (T,), _F32),
           ("loss", loss, (T,), _F32), ("loss_sum", loss_sum, (1,), _F32), ("lse", lse, (T,), _F32),
           ("dlogits", dlogits, (T, v), None), _ws_spec(ws), _status_spec(dev_status))
+    loss, lse = _row_outputs(T, dev, loss, lse)
+    loss_sum = torch.empty(1, dtype=torch.float32, device=dev) if loss_sum is None else loss_sum
+    if with_grad and dlogits is None:
+        dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
     ws, wsb = _workspace(ws, OP_DISTILL, T, K, v, N, dev)
     _check(_launch(lib().vp_distill, dev, _ptr(logits), _dt(logits), _ptr(teacher_ids),
                    _ptr(teacher_logits), _ptr(weight), T, v, K, N, 1 if renormalize else 0,
@@ -815,14 +815,14 @@ def tp_linear_logprobs_fwd(H, E, targets, N, *, scale=1.0, logprob=None, entropy
     dev = H.device
     if targets is None and logprob is not None:
         raise ValueError("logprob needs targets")
-    if targets is None:
-        entropy, lse = _row_outputs(T, dev, entropy, lse)
-    else:
-        logprob, entropy, lse = _row_outputs(T, dev, logprob, entropy, lse)
     _contig(H, E, targets, logprob, entropy, lse)
     _want(dev, ("H", H, (T, h), _BF), ("E", E, (v, h), _BF), ("targets", targets, (T,), _I64T),
           ("logprob", logprob, (T,), _F32), ("entropy", entropy, (T,), _F32),
           ("lse", lse, (T,), _F32), _ws_spec(ws), _status_spec(dev_status))
+    if targets is None:
+        entropy, lse = _row_outputs(T, dev, entropy, lse)
+    else:
+        logprob, entropy, lse = _row_outputs(T, dev, logprob, entropy, lse)
     ws, wsb = _workspace(ws, OP_LINEAR_LOGPROBS, T, h, v, N, dev)
     _check(_launch(lib().tp_linear_logprobs_fwd, dev, _ptr(H), _ptr(E), _ptr(targets), T, h, v,
                    N, float(scale), _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(ws), wsb,
