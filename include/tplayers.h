@@ -665,8 +665,10 @@ TP_API tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teac
  *   [TP-ILL] §4.2 and §5, as tp_linear_xent_fwd.
  *
  *   logprob, entropy and lse of vp_logprobs_fwd for logits = H·Eᵀ, from the
- *   GEMM's fp32 accumulators: every 128-column slice of every row leaves its
- *   maximum, Σ e and Σ e·(l − max), and a second kernel combines them.
+ *   GEMM's fp32 accumulators (K in chunks of 1024, added up in fp32; one or two
+ *   tokens on a kernel that reads E once, in fp32): every slice of columns of
+ *   every row leaves its maximum, Σ e and Σ e·(l − max), and a second kernel
+ *   combines them.
  *   H [T,h] bf16, E [v,h] bf16, h % 8 == 0, any v with v % N == 0; targets
  *   [T] int64, NULL when logprob is NULL; each output nullable, at least one
  *   given.  Out-of-range targets as in vp_logprobs_fwd.

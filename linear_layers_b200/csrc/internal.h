@@ -172,9 +172,20 @@ tp_status logprobs_bwd_launch(const LogprobsBwdArgs& a, tp_dtype dt, tp_dtype gr
                               cudaStream_t stream);
 tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_s,
                                          const float* stat_u, const float* tgt_logit,
-                                         const int64_t* targets, int64_t T, int64_t v, float scale,
-                                         float* logprob, float* entropy, float* lse,
-                                         int32_t* dev_status, cudaStream_t stream);
+                                         const int64_t* targets, int64_t T, int64_t v,
+                                         int nslices, float scale, float* logprob, float* entropy,
+                                         float* lse, int32_t* dev_status, cudaStream_t stream);
+// The statistics for one or two tokens, in slices of kFewSlice columns.
+constexpr int kFewTokens = 2;
+constexpr int kFewSlice = 32;
+tp_status linear_logprobs_few_launch(const void* H, const void* E, const int64_t* targets,
+                                     int64_t T, int64_t h, int64_t v, float scale, float* stat_m,
+                                     float* stat_s, float* stat_u, float* tgt_logit,
+                                     cudaStream_t stream);
+inline int linear_logprobs_slices(int64_t T, int64_t v) {
+  const int64_t slice = T <= kFewTokens ? kFewSlice : kXentSlice;
+  return static_cast<int>((v + slice - 1) / slice);
+}
 
 // Distillation from a teacher's top entries: see vp_distill.
 constexpr int kDistillMaxK = 256;

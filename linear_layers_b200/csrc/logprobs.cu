@@ -551,15 +551,117 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
   if (edge >= 0) put(out + edge, grad2(edge_x, 0.0f).x + (edge == y ? at_y : 0.0f));
 }
 
-// Combine of the per-slice statistics of the output-layer GEMM (slice k of
+// One or two tokens: the statistics of H·Eᵀ straight from one pass over E,
+// which is all there is to read (2 bytes and 2·T operations a weight: CUDA
+// cores keep up).  A warp takes four rows of E at once, its lanes 16-byte units
+// along h; H comes from L1.  A block's 32 columns are one slice of the
+// statistics that the combine below joins.  T = 1, h = 4096: v = 50304 takes 68
+// us, v = 100000 127 us, 6.5 TB/s; on the tensor cores, whose tiles read the one
+// row of H in every block, 93 and 155 us.  T = 3 and 4 were 88 to 95 and 159 to
+// 165 us either way.
+constexpr int kFewRows = 4;
+constexpr int kFewPerWarp = kFewSlice / kBwdWarps;
+
+template <int NT>
+__global__ void __launch_bounds__(kBwdThreads, 4)
+    linear_logprobs_few_kernel(const __nv_bfloat16* __restrict__ H,
+                               const __nv_bfloat16* __restrict__ E,
+                               const int64_t* __restrict__ targets, int64_t v, int h,
+                               float scale, float* stat_m, float* stat_s, float* stat_u,
+                               float* tgt_logit) {
+  static_assert(NT <= kBwdWarps && kFewSlice % 32 == 0 && kFewPerWarp % kFewRows == 0, "");
+  __shared__ float logit[NT][kFewSlice];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kFewSlice;
+#pragma unroll 1
+  for (int g = 0; g < kFewPerWarp; g += kFewRows) {
+    const int c = warp * kFewPerWarp + g;
+    const __nv_bfloat16* e[kFewRows];   // rows past the table: the last one, unused
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i) e[i] = E + min(col0 + c + i, v - 1) * h;
+    float2 acc[kFewRows][NT];
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[i][t] = make_float2(0.0f, 0.0f);
+#pragma unroll NT == 1 ? 2 : 1
+    for (int k = lane * 8; k < h; k += 256) {
+      uint4 w[kFewRows];
+#pragma unroll
+      for (int i = 0; i < kFewRows; ++i) w[i] = ld_unit(e[i] + k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float x[8];
+        Unit<__nv_bfloat16>::unpack(
+            __ldg(reinterpret_cast<const uint4*>(H + static_cast<int64_t>(t) * h + k)), x);
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i) {
+          float y[8];
+          Unit<__nv_bfloat16>::unpack(w[i], y);
+#pragma unroll
+          for (int q = 0; q < 8; q += 2)
+            acc[i][t] = __ffma2_rn(make_float2(x[q], x[q + 1]), make_float2(y[q], y[q + 1]), acc[i][t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float z = acc[i][t].x + acc[i][t].y;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+        if (lane == 0) logit[t][c + i] = z;
+      }
+  }
+  __syncthreads();
+  if (warp >= NT) return;
+  // one token per warp
+  constexpr int kQ = kFewSlice / 32;
+  const int t = warp;
+  const float sl = scale * kLog2e;
+  const int64_t y = targets ? targets[t] : -1;
+  float x[kQ];
+  float m = -CUDART_INF_F;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    const int64_t col = col0 + lane + 32 * q;
+    x[q] = col < v ? logit[t][lane + 32 * q] : -CUDART_INF_F;
+    if (col == y) tgt_logit[t] = x[q];
+    m = fmaxf(m, x[q]);
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float ref = m == -CUDART_INF_F ? 0.0f : m;
+  float s = 0.0f, u = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    const float d = x[q] - ref;
+    const float e = ex2_approx(d * sl);
+    s += e;
+    u = fmaf(e, max_nan(d, kLowest), u);
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, off);
+    u += __shfl_xor_sync(0xffffffffu, u, off);
+  }
+  if (lane == 0) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * NT + t;
+    stat_m[at] = m;
+    stat_s[at] = s;
+    stat_u[at] = u;
+  }
+}
+
+// Combine of the per-slice statistics of the output layer (slice k of
 // row t at [k·T + t]): M = max m_k, w_k = exp(scale·(m_k − M)),
 // S = Σ w_k·s_k, U = Σ w_k·(u_k + (m_k − M)·s_k).  A block takes eight tokens
-// (a 32-byte sector of each slice's row of numbers) and 32 slices at a time;
-// the partial results meet in a fixed order.  One token per lane and eight
-// slices at a time took 25 us of a T = 500, v = 50304 call, this takes 4.
-constexpr int kCombTokens = 8;
-constexpr int kCombSlices = kBwdThreads / kCombTokens;
-
+// (a 32-byte sector of each slice's row of numbers) and 32 slices at a time, or
+// one of few tokens and 256 slices; the partial results meet in a fixed order.
+// One token per lane and eight slices at a time took 25 us of a T = 500,
+// v = 50304 call, this takes 4.
+template <int kTokens>
 __global__ void __launch_bounds__(kBwdThreads)
     linear_logprobs_combine_kernel(const float* __restrict__ stat_m,
                                    const float* __restrict__ stat_s,
@@ -569,22 +671,23 @@ __global__ void __launch_bounds__(kBwdThreads)
                                    int nslices, float scale, float* __restrict__ logprob,
                                    float* __restrict__ entropy, float* __restrict__ lse,
                                    int32_t* dev_status) {
-  __shared__ float part_m[kBwdWarps][kCombTokens];
-  __shared__ float part_s[kBwdWarps][kCombTokens];
-  __shared__ float part_u[kBwdWarps][kCombTokens];
+  constexpr int kSlices = kBwdThreads / kTokens;
+  __shared__ float part_m[kBwdWarps][kTokens];
+  __shared__ float part_s[kBwdWarps][kTokens];
+  __shared__ float part_u[kBwdWarps][kTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tok = lane & (kCombTokens - 1);
-  const int first = threadIdx.x / kCombTokens;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kCombTokens + tok;
+  const int tok = lane & (kTokens - 1);
+  const int first = threadIdx.x / kTokens;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + tok;
   const bool ok = t < T;
   float m = -CUDART_INF_F;
   if (ok) {
 #pragma unroll 8
-    for (int k = first; k < nslices; k += kCombSlices) m = fmaxf(m, stat_m[k * T + t]);
+    for (int k = first; k < nslices; k += kSlices) m = fmaxf(m, stat_m[k * T + t]);
   }
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-  if (lane < kCombTokens) part_m[warp][tok] = m;
+#pragma unroll
+  for (int off = kTokens; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane < kTokens) part_m[warp][tok] = m;
   __syncthreads();
   float M = part_m[0][tok];
 #pragma unroll
@@ -593,7 +696,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   float S = 0.0f, U = 0.0f;
   if (ok) {
 #pragma unroll 4
-    for (int k = first; k < nslices; k += kCombSlices) {
+    for (int k = first; k < nslices; k += kSlices) {
       const float d = stat_m[k * T + t] - M;
       const float f = ex2_approx(d * (scale * kLog2e));
       const float s = stat_s[k * T + t];
@@ -602,16 +705,16 @@ __global__ void __launch_bounds__(kBwdThreads)
     }
   }
 #pragma unroll
-  for (int off = 8; off <= 16; off <<= 1) {
+  for (int off = kTokens; off <= 16; off <<= 1) {
     S += __shfl_xor_sync(0xffffffffu, S, off);
     U += __shfl_xor_sync(0xffffffffu, U, off);
   }
-  if (lane < kCombTokens) {
+  if (lane < kTokens) {
     part_s[warp][tok] = S;
     part_u[warp][tok] = U;
   }
   __syncthreads();
-  if (threadIdx.x < kCombTokens && ok) {
+  if (threadIdx.x < kTokens && ok) {
     S = 0.0f;
     U = 0.0f;
 #pragma unroll
@@ -715,13 +818,33 @@ tp_status logprobs_bwd_launch(const LogprobsBwdArgs& a, tp_dtype dt, tp_dtype gr
 
 tp_status linear_logprobs_combine_launch(const float* stat_m, const float* stat_s,
                                          const float* stat_u, const float* tgt_logit,
-                                         const int64_t* targets, int64_t T, int64_t v, float scale,
-                                         float* logprob, float* entropy, float* lse,
-                                         int32_t* dev_status, cudaStream_t stream) {
-  const int nslices = static_cast<int>((v + kXentSlice - 1) / kXentSlice);
-  linear_logprobs_combine_kernel<<<static_cast<unsigned>((T + kCombTokens - 1) / kCombTokens),
-                                   kBwdThreads, 0, stream>>>(stat_m, stat_s, stat_u, tgt_logit, targets, T, v,
-                                             nslices, scale, logprob, entropy, lse, dev_status);
+                                         const int64_t* targets, int64_t T, int64_t v,
+                                         int nslices, float scale, float* logprob, float* entropy,
+                                         float* lse, int32_t* dev_status, cudaStream_t stream) {
+  auto launch = [&](auto kernel, int tokens) {
+    kernel<<<static_cast<unsigned>((T + tokens - 1) / tokens), kBwdThreads, 0, stream>>>(
+        stat_m, stat_s, stat_u, tgt_logit, targets, T, v, nslices, scale, logprob, entropy, lse,
+        dev_status);
+  };
+  if (T <= kFewTokens) launch(linear_logprobs_combine_kernel<1>, 1);
+  else launch(linear_logprobs_combine_kernel<8>, 8);
+  note_launches(1);
+  return last_error();
+}
+
+tp_status linear_logprobs_few_launch(const void* H, const void* E, const int64_t* targets,
+                                     int64_t T, int64_t h, int64_t v, float scale, float* stat_m,
+                                     float* stat_s, float* stat_u, float* tgt_logit,
+                                     cudaStream_t stream) {
+  auto launch = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>((v + kFewSlice - 1) / kFewSlice), kBwdThreads, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(H), static_cast<const __nv_bfloat16*>(E), targets, v,
+        static_cast<int>(h), scale, stat_m, stat_s, stat_u, tgt_logit);
+  };
+  static_assert(kFewTokens == 2, "one instance for each number");
+  if (T == 1) launch(linear_logprobs_few_kernel<1>);
+  else if (T == 2) launch(linear_logprobs_few_kernel<2>);
+  else return TP_ERR_UNSUPPORTED;
   note_launches(1);
   return last_error();
 }

@@ -182,9 +182,13 @@ size_t linear_xent_ws_bytes(int64_t T, int64_t v) {
   return 3 * plane + align256(static_cast<size_t>(T) * 4);
 }
 
-// slice maxima, slice sums, slice sums of e·(x − max) ([ceil(v/128), T] each), target logits [T]:
-// the same planes as linear_xent_ws_bytes, with the third of floats
-size_t linear_logprobs_ws_bytes(int64_t T, int64_t v) { return linear_xent_ws_bytes(T, v); }
+// slice maxima, slice sums, slice sums of e·(x − max) ([slices, T] each), target logits [T]
+size_t linear_logprobs_plane(int64_t T, int64_t v) {
+  return align256(static_cast<size_t>(linear_logprobs_slices(T, v)) * T * 4);
+}
+size_t linear_logprobs_ws_bytes(int64_t T, int64_t v) {
+  return 3 * linear_logprobs_plane(T, v) + align256(static_cast<size_t>(T) * 4);
+}
 
 // A softmax scale (inverse temperature): finite and positive.
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
@@ -883,24 +887,36 @@ tp_status tp_linear_logprobs_fwd(const void* H, const void* E, const int64_t* ta
   if (ws == nullptr || ws_bytes < need) return TP_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) & 255) return TP_ERR_ALIGN;
   if (tp_status s = require_sm100()) return s;
-  const size_t plane = align256(static_cast<size_t>((v + kXentSlice - 1) / kXentSlice) * T * 4);
+  const size_t plane = linear_logprobs_plane(T, v);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  GemmProblem g;
-  g.A = H; g.lda = h; g.a_mn = 0;
-  g.B = E; g.ldb = h; g.b_mn = 0;               // E [v,h] read as Eᵀ: K-major
-  g.M = static_cast<int>(T); g.N = static_cast<int>(v); g.K = static_cast<int>(h);
-  g.epi = EPI_LOGP_STATS;
-  g.targets = targets;
-  g.logit_scale = scale;
-  g.stat_m = reinterpret_cast<float*>(w);
-  g.stat_s = reinterpret_cast<float*>(w + plane);
-  g.stat_u = reinterpret_cast<float*>(w + 2 * plane);
-  g.tgt_logit = reinterpret_cast<float*>(w + 3 * plane);
-  g.dev_status = dev_status;
+  float* stat_m = reinterpret_cast<float*>(w);
+  float* stat_s = reinterpret_cast<float*>(w + plane);
+  float* stat_u = reinterpret_cast<float*>(w + 2 * plane);
+  float* tgt_logit = reinterpret_cast<float*>(w + 3 * plane);
   cudaStream_t st = as_stream(stream);
-  if (tp_status s = gemm_tc_launch(g, st)) return s;
-  return linear_logprobs_combine_launch(g.stat_m, g.stat_s, g.stat_u, g.tgt_logit, targets, T, v,
-                                        scale, logprob, entropy, lse, dev_status, st);
+  tp_status s;
+  if (T <= kFewTokens) {
+    s = linear_logprobs_few_launch(H, E, targets, T, h, v, scale, stat_m, stat_s, stat_u,
+                                   tgt_logit, st);
+  } else {
+    GemmProblem g;
+    g.A = H; g.lda = h; g.a_mn = 0;
+    g.B = E; g.ldb = h; g.b_mn = 0;               // E [v,h] read as Eᵀ: K-major
+    g.M = static_cast<int>(T); g.N = static_cast<int>(v); g.K = static_cast<int>(h);
+    g.epi = EPI_LOGP_STATS;
+    g.targets = targets;
+    g.logit_scale = scale;
+    g.stat_m = stat_m;
+    g.stat_s = stat_s;
+    g.stat_u = stat_u;
+    g.tgt_logit = tgt_logit;
+    g.dev_status = dev_status;
+    s = gemm_tc_launch(g, st);
+  }
+  if (s) return s;
+  return linear_logprobs_combine_launch(stat_m, stat_s, stat_u, tgt_logit, targets, T, v,
+                                        linear_logprobs_slices(T, v), scale, logprob, entropy,
+                                        lse, dev_status, st);
 }
 
 tp_status tp_linear_logprobs_dlogits(const void* H, const void* E, const int64_t* targets,

@@ -86,6 +86,52 @@ def test_hidden_sizes_around_the_accumulation_chunk(T, v, h):
     assert_close("dlogits", d, O.logprobs_bwd(L, y, g, g), TOL_BF16)
 
 
+@pytest.mark.parametrize("T", [1, 2, 3])
+@pytest.mark.parametrize("v,h", [(1, 8), (31, 16), (33, 264), (1003, 1608), (50257, 512), (70, 8192)])
+def test_one_and_two_tokens(T, v, h):
+    """Slices that end inside the table, rows of H shorter than a warp's reach,
+    every output alone, a target outside the vocabulary."""
+    H, E, y = _inputs(T, v, h, seed=v + h)
+    Hd, Ed, yd = H.cuda(), E.cuda(), y.cuda()
+    ref = O.logprobs(O.logits(H, E), y, 1.25)
+    bufs, guards = {}, []
+    for k in ("logprob", "entropy", "lse"):
+        bufs[k], g = guarded((T,), torch.float32)
+        guards.append(g)
+    st = tpl.new_status()
+    need = tpl.tp_workspace_bytes(tpl.OP_LINEAR_LOGPROBS, T, h, v, 1)
+    ws, g = guarded((need,), torch.uint8, fill=0xFF)
+    guards.append(g)
+    r = tpl.tp_linear_logprobs_fwd(Hd, Ed, yd, 1, scale=1.25, ws=ws, dev_status=st, **bufs)
+    for g in guards:
+        g.check()
+    _check_fwd(r, ref)
+    assert int(st.item()) == 0
+    again = tpl.tp_linear_logprobs_fwd(Hd, Ed, yd, 1, scale=1.25)
+    for k in bufs:
+        assert torch.equal(r[k], again[k]), k
+    bare = tpl.tp_linear_logprobs_fwd(Hd, Ed, None, 1, scale=1.25)
+    assert torch.equal(bare["lse"], r["lse"]) and torch.equal(bare["entropy"], r["entropy"])
+    yd[T - 1] = v
+    bad = tpl.tp_linear_logprobs_fwd(Hd, Ed, yd, 1, scale=1.25, dev_status=st)
+    assert int(st.item()) == tpl.DEVERR_RANGE
+    assert torch.isnan(bad["logprob"][T - 1]) and torch.equal(bad["lse"], r["lse"])
+    assert torch.equal(bad["logprob"][:T - 1], r["logprob"][:T - 1])
+
+
+def test_one_token_with_infinite_and_nan_logits():
+    H = torch.ones(1, 64).bfloat16()
+    E = (torch.randn(100, 64, generator=torch.Generator().manual_seed(4)) * 0.1).bfloat16()
+    y = torch.tensor([7])
+    E[40, 3] = -math.inf                          # a token of probability 0
+    r = tpl.tp_linear_logprobs_fwd(H.cuda(), E.cuda(), y.cuda(), 1)
+    _check_fwd(r, O.logprobs(O.logits(H, E), y))
+    E[41, 5] = math.nan
+    r = tpl.tp_linear_logprobs_fwd(H.cuda(), E.cuda(), y.cuda(), 1)
+    for k in ("logprob", "entropy", "lse"):
+        assert torch.isnan(r[k]).all(), k
+
+
 def test_long_sums_of_one_sign():
     """Logits of 16 as 65536 positive products.  Within a chunk of 1024 the
     tensor core adds 64 times and truncates by at most 2^-22 of the sum so far;
