@@ -167,7 +167,7 @@ constexpr int kUnits = 4;           // 16-byte units per thread and step
 // many instructions for half the bytes: 140 us, 5.9 TB/s.
 template <typename IT, bool kTop>
 __global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
-    logprobs_kernel(const LogprobsArgs a, int slices) {
+    logprobs_kernel(const LogprobsArgs a, int slices, int group_log) {
   constexpr int kN = Unit<IT>::kN;
   using Cand = Candidates;
   extern __shared__ __align__(16) uint8_t dyn_smem[];
@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
   const RowShape<IT> shape(f0, a.v);
   const IT* row = static_cast<const IT*>(a.logits) + f0;
   const IT* body = row + shape.head;
-  const int per = (shape.units + slices - 1) / slices;
-  const int u0 = min(rank * per, shape.units), u1 = min(u0 + per, shape.units);
+  const Part part(shape.units, rank, slices);
+  const int u0 = part.first, u1 = part.last;
   const int tid = threadIdx.x;
   const float sl = a.scale * kLog2e;
   const float tau = 8.0f / sl;
@@ -217,13 +217,11 @@ __global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
   RowSums sums;
   uint4 next[kUnits];
   load(u0, next);
-  const int steps = (u1 - u0 + kThreads * kUnits - 1) / (kThreads * kUnits);
-  // groups of 2^group_log steps, at most kGroups of them
-  int group_log = 0;
-  if constexpr (kTop)
-    while ((Cand::kGroups << group_log) < steps) ++group_log;
+  const int steps = steps_of(u1 - u0, kThreads * kUnits);
+  // groups of 2^group_log steps: no more than the launch has room for, whose
+  // group_log is the widest block's
   const int group_steps = kTop ? 1 << group_log : max(steps, 1);
-  const int groups = kTop ? (steps + group_steps - 1) >> group_log : min(steps, 1);
+  const int groups = kTop ? groups_of(steps, group_log) : min(steps, 1);
   [[maybe_unused]] bool lane_has = false;   // the lane's first element is there and a number
   if constexpr (kTop) {
     float x[kN];
@@ -748,20 +746,18 @@ tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
   // v = 50304, fp32: 128 rows on 1, 4, 8 blocks each take 13.9, 6.8, 8.0 us, 512
   // rows on 1, 2, 4 take 32.7, 21.4, 24.8; with 20 alternatives, whose joining
   // costs more, 16.7, 13.0, 15.6 and 29.4, 25.3, 34.7.
-  const int64_t units = a.v / Unit<IT>::kN;
+  const int units = static_cast<int>(a.v / Unit<IT>::kN);   // of the widest row
   const int64_t most = (kTop ? 4 : 7) * num_sms();
   int slices = 1;
   while (slices < 8 && a.T * slices * 2 <= most && units / (slices * 2) >= 2 * kThreads)
     slices *= 2;
   size_t smem = 0;
+  int group_log = 0;
   if constexpr (kTop) {
     using Cand = Candidates;
-    const int64_t per = (units + slices - 1) / slices;
-    const int64_t steps = (per + kUnits * kThreads - 1) / (kUnits * kThreads);
-    int log = 0;
-    while ((static_cast<int64_t>(Cand::kGroups) << log) < steps) ++log;
-    const int64_t groups = (steps + (1 << log) - 1) >> log;
-    smem = sizeof(Cand) + (groups + 3) / 4 * kThreads * sizeof(float4);
+    const int steps = steps_of(Part(units, 0, slices).last, kThreads * kUnits);
+    group_log = group_log_of(steps, Cand::kGroups);
+    smem = sizeof(Cand) + (groups_of(steps, group_log) + 3) / 4 * kThreads * sizeof(float4);
     static_assert(Cand::kGroups <= 32 && sizeof(Cand) + Cand::kGroups * kThreads * sizeof(float) <= 48 * 1024,
                   "within the default limit of dynamic shared memory");
     static_assert(Cand::kRoom >= 8 * kLogprobsMaxK, "room for the slices' best");
@@ -778,7 +774,7 @@ tp_status logprobs_fwd_launch_t(const LogprobsArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = slices > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, logprobs_kernel<IT, kTop>, a, slices) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, logprobs_kernel<IT, kTop>, a, slices, group_log) != cudaSuccess) {
     cudaGetLastError();
     return TP_ERR_CUDA;
   }

@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "row_split.h"
 #include "sm100_ptx.cuh"
 
 namespace tpl {
@@ -93,21 +94,8 @@ __device__ __forceinline__ void put_unit(__nv_bfloat16* p, const float* x) {
                       pack_bf16x2(x[6], x[7])));
 }
 
-// A row of v elements from flat element f0 of a 16-byte-aligned matrix: `head`
-// elements up to the first 16-byte boundary, `units` whole units, `tail`.
-// Rows of any length are read in aligned units this way, and nothing outside
-// the row is touched.
 template <typename IT>
-struct RowShape {
-  int head, units, tail;
-  __device__ __forceinline__ RowShape(int64_t f0, int64_t v) {
-    constexpr int n = Unit<IT>::kN;
-    head = static_cast<int>((-f0) & (n - 1));
-    if (head > v) head = static_cast<int>(v);
-    units = static_cast<int>((v - head) / n);
-    tail = static_cast<int>(v - head) - units * n;
-  }
-};
+using RowShape = RowSplit<Unit<IT>::kN>;
 
 // Running softmax sums of one thread over raw logits: s = Σ e, u = Σ e·(x − r)
 // with e = exp(scale·(x − r)).  The reference r moves only when a logit
