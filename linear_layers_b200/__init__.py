@@ -782,12 +782,15 @@ def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weig
                loss_sum=None, lse=None, dlogits=None, ws=None, dev_status=None):
     """Loss of softmax(scale·logits) against a teacher's listed entries (ids [T, K] int32, −1 for
     an empty slot; logits [T, K] fp32, or log-probabilities with renormalize=False), and its
-    gradient at the logits in grad_dtype (or the type of ``dlogits``).
+    gradient at the logits in grad_dtype (or the type of ``dlogits``, which is refused with
+    with_grad=False).
 
     Returns {"loss" [T], "loss_sum" [1], "lse" [T], "dlogits" [T, v] or None}."""
     T, v = logits.shape
     dev = logits.device
     K = teacher_ids.shape[1]
+    if dlogits is not None and not with_grad:
+        raise ValueError("dlogits needs with_grad")
     _contig(logits, teacher_ids, teacher_logits, weight, loss, loss_sum, lse, dlogits)
     _want(dev, ("teacher_ids", teacher_ids, (T, K), _I32T),
           ("teacher_logits", teacher_logits, (T, K), _F32), ("weight", weight, (T,), _F32),
