@@ -149,12 +149,16 @@ def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _dt(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _dtype_code(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return DTYPE_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return DTYPE_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _dt(t: torch.Tensor) -> int:
+    return _dtype_code(t.dtype)
 
 
 def _offsets(offsets, N):
@@ -714,6 +718,7 @@ def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, ent
           ("entropy", entropy, (T,), _F32), ("lse", lse, (T,), _F32),
           ("top_idx", top_idx, (T, top_k), _I32T), ("top_logprob", top_logprob, (T, top_k), _F32),
           _status_spec(dev_status))
+    dt = _dt(logits)
     if targets is None:
         entropy, lse = _row_outputs(T, dev, entropy, lse)
     else:
@@ -723,7 +728,7 @@ def vp_logprobs_fwd(logits, targets, N, *, scale=1.0, top_k=0, logprob=None, ent
             top_idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
         if top_logprob is None:
             top_logprob = torch.empty(T, top_k, dtype=torch.float32, device=dev)
-    _check(_launch(lib().vp_logprobs_fwd, dev, _ptr(logits), _dt(logits), _ptr(targets), T, v,
+    _check(_launch(lib().vp_logprobs_fwd, dev, _ptr(logits), dt, _ptr(targets), T, v,
                    N, float(scale), int(top_k), _ptr(logprob), _ptr(entropy), _ptr(lse),
                    _ptr(top_idx), _ptr(top_logprob), _ptr(dev_status)), "vp_logprobs_fwd")
     return {"logprob": logprob, "entropy": entropy, "lse": lse, "top_idx": top_idx,
@@ -763,17 +768,17 @@ def vp_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, N, *, sca
     T, v = logits.shape
     dev = logits.device
     _logprob_grad_args(targets, entropy, dlogprob, dentropy)
-    if dlogits is None:
-        dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
     _contig(logits, targets, lse, entropy, dlogprob, dentropy, dlogits)
     _want(dev, ("targets", targets, (T,), _I64T), ("lse", lse, (T,), _F32),
           ("entropy", entropy, (T,), _F32), ("dlogprob", dlogprob, (T,), _F32),
           ("dentropy", dentropy, (T,), _F32), ("dlogits", dlogits, (T, v), None),
           _status_spec(dev_status))
-    _check(_launch(lib().vp_logprobs_bwd, dev, _ptr(logits), _dt(logits), _ptr(targets),
-                   _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy), T, v, N,
-                   float(scale), _ptr(dlogits), _dt(dlogits), _ptr(dev_status)),
-                   "vp_logprobs_bwd")
+    dt, grad_dt = _dt(logits), _dtype_code(grad_dtype if dlogits is None else dlogits.dtype)
+    if dlogits is None:
+        dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
+    _check(_launch(lib().vp_logprobs_bwd, dev, _ptr(logits), dt, _ptr(targets), _ptr(lse),
+                   _ptr(entropy), _ptr(dlogprob), _ptr(dentropy), T, v, N, float(scale),
+                   _ptr(dlogits), grad_dt, _ptr(dev_status)), "vp_logprobs_bwd")
     return dlogits
 
 
@@ -796,16 +801,19 @@ def vp_distill(logits, teacher_ids, teacher_logits, N, *, renormalize=True, weig
           ("teacher_logits", teacher_logits, (T, K), _F32), ("weight", weight, (T,), _F32),
           ("loss", loss, (T,), _F32), ("loss_sum", loss_sum, (1,), _F32), ("lse", lse, (T,), _F32),
           ("dlogits", dlogits, (T, v), None), _ws_spec(ws), _status_spec(dev_status))
+    dt = _dt(logits)
+    grad_dt = DTYPE_BF16
+    if with_grad:
+        grad_dt = _dtype_code(grad_dtype if dlogits is None else dlogits.dtype)
     loss, lse = _row_outputs(T, dev, loss, lse)
     loss_sum = torch.empty(1, dtype=torch.float32, device=dev) if loss_sum is None else loss_sum
     if with_grad and dlogits is None:
         dlogits = torch.empty(T, v, dtype=grad_dtype, device=dev)
     ws, wsb = _workspace(ws, OP_DISTILL, T, K, v, N, dev)
-    _check(_launch(lib().vp_distill, dev, _ptr(logits), _dt(logits), _ptr(teacher_ids),
+    _check(_launch(lib().vp_distill, dev, _ptr(logits), dt, _ptr(teacher_ids),
                    _ptr(teacher_logits), _ptr(weight), T, v, K, N, 1 if renormalize else 0,
                    float(scale), float(grad_scale), _ptr(loss), _ptr(loss_sum), _ptr(lse),
-                   _ptr(dlogits), DTYPE_BF16 if dlogits is None else _dt(dlogits), _ptr(ws),
-                   wsb, _ptr(dev_status)), "vp_distill")
+                   _ptr(dlogits), grad_dt, _ptr(ws), wsb, _ptr(dev_status)), "vp_distill")
     return {"loss": loss, "loss_sum": loss_sum, "lse": lse, "dlogits": dlogits}
 
 
@@ -841,12 +849,13 @@ def tp_linear_logprobs_dlogits(H, E, targets, lse, entropy, dlogprob, dentropy, 
     v = E.shape[0]
     dev = H.device
     _logprob_grad_args(targets, entropy, dlogprob, dentropy)
-    dlogits = torch.empty(T, v, dtype=torch.bfloat16, device=dev) if dlogits is None else dlogits
     _contig(H, E, targets, lse, entropy, dlogprob, dentropy, dlogits)
     _want(dev, ("H", H, (T, h), _BF), ("E", E, (v, h), _BF), ("targets", targets, (T,), _I64T),
           ("lse", lse, (T,), _F32), ("entropy", entropy, (T,), _F32),
           ("dlogprob", dlogprob, (T,), _F32), ("dentropy", dentropy, (T,), _F32),
           ("dlogits", dlogits, (T, v), _BF), _status_spec(dev_status))
+    if dlogits is None:
+        dlogits = torch.empty(T, v, dtype=torch.bfloat16, device=dev)
     _check(_launch(lib().tp_linear_logprobs_dlogits, dev, _ptr(H), _ptr(E), _ptr(targets),
                    _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy), T, h, v, N,
                    float(scale), _ptr(dlogits), _ptr(dev_status)), "tp_linear_logprobs_dlogits")
