@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32)
     distill_slots_kernel(const DistillArgs a, int2* __restrict__ entries,
                          float4* __restrict__ info) {
   constexpr int kSeenWords = 128 * S;   // 128 bits for every slot, to notice a token listed twice
-  __shared__ uint32_t seen_bits[kPrepWarps][kSeenWords];
+  __shared__ __align__(16) uint32_t seen_bits[kPrepWarps][kSeenWords];   // cleared 16 bytes at a time
   __shared__ int2 listed[kPrepWarps][32 * S];
   grid_dependents_launch();   // the rows' kernel reads nothing of this one before it has ended
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
