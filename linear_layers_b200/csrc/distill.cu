@@ -648,8 +648,10 @@ tp_status launch(const DistillArgs& a, const Slots& slots, int slices, int per,
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kMost > kSmem ? kMost : kSmem)) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
+      cudaGetLastError();
       return TP_ERR_CUDA;
+    }
     configured[dev & 63] = true;
   }
   cudaLaunchConfig_t cfg = {};

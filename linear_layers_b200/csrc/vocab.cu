@@ -538,8 +538,10 @@ tp_status loss_sum_launch(const float* loss, int64_t T, float* loss_sum, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = early ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, loss_sum_kernel, loss, T, loss_sum) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, loss_sum_kernel, loss, T, loss_sum) != cudaSuccess) {
+    cudaGetLastError();
     return TP_ERR_CUDA;
+  }
   note_launches(1);
   return TP_OK;
 }
