@@ -98,13 +98,32 @@ template <typename IT>
 using RowShape = RowSplit<Unit<IT>::kN>;
 
 // Running softmax sums of one thread over raw logits: s = Σ e, u = Σ e·(x − r)
-// with e = exp(scale·(x − r)).  The reference r moves only when a logit
-// exceeds it by more than 8 in log2 units, so e stays below 2^8 and the
-// rescaling is rare; any reference gives the same result.  A thread that has
-// seen no logit above −inf keeps r = 0 with the threshold at −inf.
+// with e = exp(scale·(x − r)).  Any reference r gives the same sums but for
+// their rounding: with r a distance δ = scale·(M − r) below the row's maximum,
+// entropy = log S − scale·U/S is a difference of two numbers of size δ, whose
+// rounding errors it keeps.  r moves when a logit exceeds it by more than
+// 2 in log2 units, so δ < 1.4; within 8 (δ < 5.6) the entropies of rows whose two
+// highest logits lie 5 apart were off by up to 5.0e-6 of their size, within 2 by
+// 6.7e-7, at r = M by 5.5e-7.  A thread that has seen no logit above −inf keeps
+// r = 0 with the threshold at −inf, unless its warp started at one.
 struct RowSums {
   float ref = 0.0f, above = -INFINITY;
   float2 s = {0.0f, 0.0f}, u = {0.0f, 0.0f};
+
+  // A first reference for the whole warp, the largest of its lanes' x: the
+  // steps behind it move references less often than from one of each lane.
+  template <int N>
+  __device__ __forceinline__ void start(const float (&x)[N], float tau) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (m > -INFINITY) {
+      ref = m;
+      above = m + tau;
+    }
+  }
 
   template <int N, bool kEntropy>
   __device__ __forceinline__ float add(const float (&x)[N], float sl, float tau) {
