@@ -131,6 +131,16 @@ TP_API tp_status tp_selftest_wait_timeout(int32_t* dev_status, uint32_t limit_us
  */
 TP_API tp_status tp_debug_stall_next_gemm(int32_t unit, int32_t kblock, uint32_t wait_limit_us);
 
+/*
+ * The same for the NEXT vp_distill gradient launch of this process: the copy
+ * of the first block's part of row `row` is never issued.  The waits for it
+ * run out after wait_limit_us, TP_DEVERR_TIMEOUT is set, and the call ends a
+ * few limits later however many rows remain.  Rows before `row` are right; the
+ * others may be garbage.  A row that the launch does not reach does nothing.
+ *   Returns TP_ERR_SHAPE for a negative row, or a limit of 0 or above 10 s.
+ */
+TP_API tp_status tp_debug_stall_next_distill(int64_t row, uint32_t wait_limit_us);
+
 /* Human-readable text of a status code (static storage, never NULL). */
 TP_API const char* tp_status_string(tp_status s);
 
@@ -649,9 +659,9 @@ TP_API tp_status vp_logprobs_bwd(const void* logits, tp_dtype dt, const int64_t*
  *   [−1, v) in any other row sets TP_DEVERR_RANGE and makes that row's loss
  *   and gradient NaN.  A listed token of probability above 0 whose logit is
  *   −inf gives loss +inf.  ws, ws_bytes >= tp_workspace_bytes(TP_OP_DISTILL,
- *   T, K, v, N), 16-byte aligned (the merged slots).  Waits for copies and for the other blocks of a
- *   row are bounded: if one runs out, TP_DEVERR_TIMEOUT is set and outputs
- *   are garbage.
+ *   T, K, v, N), 16-byte aligned (the merged slots).  Waits for copies and for
+ *   the other blocks of a row are bounded: if one runs out, TP_DEVERR_TIMEOUT is
+ *   set, no further wait of that block's is long, and outputs are garbage.
  */
 TP_API tp_status vp_distill(const void* logits, tp_dtype dt, const int32_t* teacher_ids,
                             const float* teacher_logits, const float* weight, int64_t T,

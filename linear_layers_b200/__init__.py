@@ -24,7 +24,7 @@ import torch
 __all__ = [
     "TPError", "lib", "library_path", "ACT_NONE", "ACT_GELU_TANH", "ACT_GELU_ERF",
     "tp_status_string", "tp_version", "tp_launch_count", "tp_selftest_wait_timeout",
-    "tp_debug_stall_next_gemm",
+    "tp_debug_stall_next_gemm", "tp_debug_stall_next_distill",
     "tp_workspace_bytes", "tp_mlp_fwd", "tp_mlp_bwd",
     "tp_col_linear_fwd", "tp_col_linear_bwd", "tp_row_linear_fwd", "tp_row_linear_bwd",
     "tp_row_linear_fwd_noalloc", "NOALLOC_SCRATCH_BYTES",
@@ -61,6 +61,7 @@ _SIGS = {
     "tp_launch_count": ([], ctypes.c_uint64),
     "tp_selftest_wait_timeout": ([_P, ctypes.c_uint32, _P], _I32),
     "tp_debug_stall_next_gemm": ([_I32, _I32, ctypes.c_uint32], _I32),
+    "tp_debug_stall_next_distill": ([_I64, ctypes.c_uint32], _I32),
     "tp_workspace_bytes": ([_I32, _I64, _I64, _I64, _I32], _SZ),
     "tp_mlp_fwd": ([_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _I32, _I32,
                     _P, _P, _P, _P, _P, _SZ, _P, _P], _I32),
@@ -239,6 +240,13 @@ def tp_debug_stall_next_gemm(unit: int, kblock: int, wait_limit_us: int = 50000)
     (diagnostics of the bounded-wait failure path; see tplayers.h)."""
     _check(lib().tp_debug_stall_next_gemm(int(unit), int(kblock), int(wait_limit_us)),
            "tp_debug_stall_next_gemm")
+
+
+def tp_debug_stall_next_distill(row: int, wait_limit_us: int = 50000):
+    """Arm the one-shot stall of the next distillation step's copy of a row (diagnostics of the
+    bounded-wait failure path; see tplayers.h)."""
+    _check(lib().tp_debug_stall_next_distill(int(row), int(wait_limit_us)),
+           "tp_debug_stall_next_distill")
 
 
 def tp_workspace_bytes(op: int, M: int, h: int, F: int, N: int) -> int:

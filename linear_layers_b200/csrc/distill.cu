@@ -17,8 +17,10 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "internal.h"
@@ -344,10 +346,15 @@ struct Held<__nv_bfloat16, R> {
 //      threads write P·q over their slice;
 //   4. the teacher warp, behind a barrier, writes the listed tokens over that;
 //      block 0's writes the loss.
+//
+// Waits are bounded, and a block of which one has run out waits no more: it
+// arms no barrier again (the last phase may be incomplete), asks for no copy and
+// sends no record, so its peers' waits run out in turn and the call ends a few
+// limits later, whatever its rows.
 template <typename IT, typename GT, int R, int NT>
 __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
     distill_kernel(const DistillArgs a, const Slots slots, int slices, int per, int nbuf,
-                   uint32_t buf_stride, uint64_t wait_ns) {
+                   uint32_t buf_stride, uint64_t wait_ns, int64_t stall_row) {
   constexpr int kN = Unit<IT>::kN;
   constexpr int kWarps = NT / 32;
   extern __shared__ __align__(128) uint8_t buffers[];       // the slices, then the slot lists
@@ -358,6 +365,8 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
   __shared__ __align__(8) uint64_t load_bar[2];
   __shared__ __align__(16) float wmax[2][kWarps], wsum[2][kWarps];   // [row parity] the warps' m, S
   __shared__ float4 row_info[2];                            // [row parity]
+  __shared__ volatile int late;    // a wait of this block has run out
+  __shared__ int asked;            // rows whose copies thread 32 has asked for
 
   const int rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t cluster = blockIdx.x / static_cast<unsigned>(slices);
@@ -367,6 +376,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
 
   grid_dependents_launch();
   if (tid == 0) {
+    late = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&rec_bar[i], 1);
       mbar_init(&own_bar[i], 1);
@@ -377,13 +387,16 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
   __syncthreads();
   if (slices > 1) cluster_sync_all();   // every barrier exists before a peer signals it
 
-  auto timeout = [&]() {
-    if (a.dev_status) atomicOr(a.dev_status, TP_DEVERR_TIMEOUT);
+  auto wait = [&](uint64_t* bar, int phase) {
+    const uint32_t parity = static_cast<uint32_t>(phase) & 1u;
+    if (mbar_test_cluster(bar, parity) || late) return;
+    if (!mbar_wait_cluster_bounded(bar, parity, wait_ns, &late)) {
+      late = 1;
+      if (a.dev_status) atomicOr(a.dev_status, TP_DEVERR_TIMEOUT);
+    }
   };
   auto wait_slice = [&](int k) {
-    if (!mbar_wait_cluster_bounded(&load_bar[nbuf == 2 ? k & 1 : 0],
-                                   static_cast<uint32_t>(nbuf == 2 ? k >> 1 : k) & 1u, wait_ns))
-      timeout();
+    wait(&load_bar[nbuf == 2 ? k & 1 : 0], nbuf == 2 ? k >> 1 : k);
   };
   // this block's sums of row k, and the row's over all slices (a whole warp
   // calls it)
@@ -402,8 +415,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
   };
   auto row_sums = [&](int k) {
     if (slices == 1) return block_sums(k);
-    if (!mbar_wait_cluster_bounded(&rec_bar[k & 1], static_cast<uint32_t>(k >> 1) & 1u, wait_ns))
-      timeout();
+    wait(&rec_bar[k & 1], k >> 1);
     const float* q = rec[k & 1][min(lane, slices - 1)];
     return join_sums(slices, Sums{q[0], q[1], 0.0f}, sl);
   };
@@ -458,7 +470,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       const int2* own = own_of[par];
       const IT* slice =
           reinterpret_cast<const IT*>(buffers + (nbuf == 2 ? par : 0) * buf_stride);
-      if (rank == 0 && lane == 0 && slices > 1)
+      if (rank == 0 && lane == 0 && slices > 1 && !late)
         mbar_arrive_expect_tx(&own_bar[par], static_cast<uint32_t>(slices) * 16u);
       wait_slice(k);
 #pragma unroll 4
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       }
       A = warp_sum(A);
       P_own = warp_sum(P_own);
-      if (slices > 1 && lane == 0)
+      if (slices > 1 && lane == 0 && !late)
         st_async_v4(mapa_shared(&own_rec[par][rank][0], 0), mapa_shared(&own_bar[par], 0), A, P_own,
                     block_ref, 0.0f);
       int n_next = 0;
@@ -496,8 +508,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       const bool dead = w == 0.0f || (P == 0.0f && !any_bad);
       if (rank == 0) {
         if (slices > 1) {   // the slices' A moved to the common reference, in slice order
-          if (!mbar_wait_cluster_bounded(&own_bar[par], static_cast<uint32_t>(k >> 1) & 1u, wait_ns))
-            timeout();
+          wait(&own_bar[par], k >> 1);
           A = 0.0f;
           for (int i = 0; i < slices; ++i) {
             const float* q = own_rec[par][i];
@@ -531,6 +542,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       const int u0 = min(rank * per, shape.units), u1 = min(u0 + per, shape.units);
       const uint32_t bytes = static_cast<uint32_t>(u1 - u0) * 16u;
       mbar_arrive_expect_tx(&load_bar[b], bytes);
+      if (t == stall_row && rank == 0) return;   // diagnostics: the copy never comes
       const char* src = static_cast<const char*>(a.logits) +
                         (t * a.v + shape.head) * static_cast<int64_t>(sizeof(IT)) +
                         static_cast<int64_t>(u0) * 16;
@@ -538,9 +550,11 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       for (uint32_t off = 0; off < bytes; off += 16384u)
         bulk_load(dst + off, src + off, min(bytes - off, 16384u), &load_bar[b]);
     };
-    if (tid == 32)
-      for (int b = 0; b < nbuf; ++b)
-        if (cluster + b * clusters < a.T) issue(b, cluster + b * clusters);
+    if (tid == 32) {
+      int n = 0;
+      for (; n < nbuf && cluster + n * clusters < a.T; ++n) issue(n, cluster + n * clusters);
+      asked = n;
+    }
     constexpr uint32_t kInf = Unit<IT>::kMinusInf;
     const uint4 fill = make_uint4(kInf, kInf, kInf, kInf);
     // the row's edges: thread i of block 0 the i-th element of the head, thread
@@ -565,7 +579,7 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       const uint4* slice =
           reinterpret_cast<const uint4*>(buffers + (nbuf == 2 ? par : 0) * buf_stride);
       // this row's records: one arrival here, 16 bytes from each slice
-      if (tid == 0 && slices > 1)
+      if (tid == 0 && slices > 1 && !late)
         mbar_arrive_expect_tx(&rec_bar[par], static_cast<uint32_t>(slices) * 16u);
       const int my_edge = edge_of(shape);
       const float edge_x = next_edge;
@@ -586,14 +600,15 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
         wsum[par][warp] = s_w;
       }
       named_barrier_sync(1, NT + 32);
-      if (tid == 32 && t + nbuf * clusters < a.T) {
+      if (tid == 32 && t + nbuf * clusters < a.T && !late) {
         fence_proxy_async_smem();
         issue(nbuf == 2 ? par : 0, t + nbuf * clusters);
+        asked = k + nbuf + 1;
       }
       next_edge = load_edge(t + clusters);
       if (slices > 1 && warp == 0) {
         const Sums own = block_sums(k);
-        if (lane < slices)
+        if (lane < slices && !late)
           st_async_v4(mapa_shared(&rec[par][rank][0], static_cast<uint32_t>(lane)),
                       mapa_shared(&rec_bar[par], static_cast<uint32_t>(lane)), own.m, own.s, 0.0f,
                       0.0f);
@@ -621,10 +636,20 @@ __global__ void __launch_bounds__(NT + 32, blocks_per_sm(R, NT))
       // the teacher warp's writes come after these; nothing here waits
       named_barrier_arrive(2, NT + 32);
     }
+    if (tid == 32 && late)   // copies that may still be on their way into this block
+      for (int r = max(asked - nbuf, 0); r < asked; ++r)
+        mbar_wait_cluster_bounded(&load_bar[nbuf == 2 ? r & 1 : 0],
+                                  static_cast<uint32_t>(nbuf == 2 ? r >> 1 : r) & 1u, wait_ns);
   }
   __syncthreads();
   if (slices > 1) cluster_sync_all();   // every peer's record into this block has landed
 }
+
+// One-shot debug injection (tp_debug_stall_next_distill) for the next launch.
+std::mutex g_stall_mu;
+int64_t g_stall_row = -1;
+uint64_t g_stall_wait_ns = 0;
+std::atomic<bool> g_stall_armed{false};
 
 // One launch: rows in slices of `per` units.
 template <typename IT, typename GT, int R, int NT>
@@ -686,10 +711,19 @@ tp_status launch(const DistillArgs& a, const Slots& slots, int slices, int per,
     last.smem = smem;
     last.clusters = n;
   }
+  int64_t stall_row = -1;
+  uint64_t wait_ns = wait_limit_ns();
+  if (g_stall_armed.load(std::memory_order_relaxed)) {
+    std::lock_guard<std::mutex> lk(g_stall_mu);
+    if (g_stall_armed.exchange(false)) {
+      stall_row = g_stall_row;
+      wait_ns = g_stall_wait_ns;
+    }
+  }
   const int64_t clusters = a.T < last.clusters ? a.T : last.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * slices));
   if (cudaLaunchKernelEx(&cfg, kernel, a, slots, slices, per, nbuf, static_cast<uint32_t>(stride),
-                         wait_limit_ns()) != cudaSuccess) {
+                         wait_ns, stall_row) != cudaSuccess) {
     cudaGetLastError();
     return TP_ERR_CUDA;
   }
@@ -749,6 +783,13 @@ void with_slots(int K, F f) {
 }
 
 }  // namespace
+
+void arm_distill_stall(int64_t row, uint64_t wait_ns) {
+  std::lock_guard<std::mutex> lk(g_stall_mu);
+  g_stall_row = row;
+  g_stall_wait_ns = wait_ns;
+  g_stall_armed = true;
+}
 
 size_t distill_ws_bytes(int64_t T, int64_t K) {
   return static_cast<size_t>(T) * (sizeof(float4) + K * sizeof(int2));

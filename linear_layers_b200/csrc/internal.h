@@ -206,6 +206,8 @@ struct DistillArgs {
   int32_t* dev_status;
 };
 size_t distill_ws_bytes(int64_t T, int64_t K);
+// Arm the one-shot debug injection of the next gradient launch.
+void arm_distill_stall(int64_t row, uint64_t wait_ns);
 tp_status distill_launch(const DistillArgs& a, tp_dtype dt, tp_dtype grad_dt, float* loss_sum,
                          void* ws, cudaStream_t stream);
 

@@ -49,3 +49,10 @@ extern "C" tp_status tp_debug_stall_next_gemm(int32_t unit, int32_t kblock, uint
   arm_gemm_injection(unit, kblock, static_cast<uint64_t>(wait_limit_us) * 1000ull);
   return TP_OK;
 }
+
+extern "C" tp_status tp_debug_stall_next_distill(int64_t row, uint32_t wait_limit_us) {
+  using namespace tpl;
+  if (row < 0 || wait_limit_us == 0 || wait_limit_us > 10000000u) return TP_ERR_SHAPE;
+  arm_distill_stall(row, static_cast<uint64_t>(wait_limit_us) * 1000ull);
+  return TP_OK;
+}
