@@ -616,7 +616,10 @@ TP_API tp_status vp_logprobs_fwd(const void* logits, tp_dtype dt, const int64_t*
  *
  *   with g = dlogprob[t] and e = dentropy[t] (fp32 [T]; either NULL: zero).
  *   lse and entropy from vp_logprobs_fwd at the same scale (entropy NULL
- *   without dentropy, targets NULL without dlogprob).  The alternatives
+ *   without dentropy, targets NULL without dlogprob).  p_j = exp(z_j − lse)
+ *   takes lse as it is given, in fp32, so p is off by up to 2^-24·|lse| of its
+ *   size: a row whose logits share an offset of millions, such as one of the
+ *   type's lowest value alone, has no gradient to speak of (give it g = e = 0).  The alternatives
  *   carry no gradient.  dlogits [T,v] bf16 or fp32 (grad_dt), 16-byte
  *   aligned; it may be the logits themselves when grad_dt == dt, and must
  *   not overlap them otherwise.

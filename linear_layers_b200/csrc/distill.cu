@@ -9,10 +9,12 @@
 //
 // Every logit is needed twice, once for S and once for the gradient.  A
 // cluster of up to eight blocks holds one row, each block its slice in
-// registers (as the exponentials, so that each is taken once) while the next
-// rows' slices arrive in shared memory: HBM sees each logit read once and each
-// gradient written once, and the writes of one row run beside the reads of
-// the next.
+// registers while the next rows' slices arrive in shared memory: HBM sees each
+// logit read once and each gradient written once, and the writes of one row run
+// beside the reads of the next.  fp32 rows are held as the exponentials, each
+// taken once; bf16 rows as they are, packed, each exponential taken twice.
+// Rows of weight 0 are read like the others (lse needs them) and written as
+// zeros.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -736,8 +738,8 @@ tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_
   constexpr int kN = Unit<IT>::kN;
   const int64_t units = (a.v + kN - 1) / kN;
   // Slices of a row: as few of 1, 2, 4, 6 and 8 as hold it.  A row of 50304 fp32
-  // logits in gradient steps of 8192 rows took 411 us on two blocks of 512
-  // threads, 643 us on eight of 128: every exchange waits for the last of the
+  // logits in gradient steps of 8192 rows takes 409 us on two blocks of 480
+  // threads (411 on two of 512) and took 643 us on eight of 128: every exchange waits for the last of the
   // row's blocks.  Clusters have to fit the GPU's processing clusters: 22 of six
   // blocks are resident, 15 of eight, 26 of five and 45 of three, and 500 fp32
   // rows of 200001 took 137, 161 and 165 us on six, eight and five, 800 rows of
@@ -756,6 +758,8 @@ tp_status distill_launch_t(const DistillArgs& a, const Slots& slots, cudaStream_
   // Units a thread x streaming threads.  480 and the teacher's warp make 16 warps
   // on four schedulers, with 128 registers each (two blocks: 64); 512 make 17,
   // with 96 (56): 777 bf16 rows of 50257 take 40.8 us on 14 x 480, 42.2 on 13 x 512.
+  // 9 x 480 spills at its 64 registers, fp32 to fp32 80 bytes a thread: 8192 rows of
+  // 16000 take 188 us (138 to bf16, which spills 16).
   if (per <= 4 * 128) return launch<IT, GT, 4, 128>(a, slots, slices, per, stream);
   if (per <= 8 * 128) return launch<IT, GT, 8, 128>(a, slots, slices, per, stream);
   if (per <= 13 * 128) return launch<IT, GT, 13, 128>(a, slots, slices, per, stream);

@@ -73,7 +73,8 @@ constexpr int kThreads = 64 + kEpiThreads;
 // us in one chain, 69.7 with chunks of 1024, 80 with 512 and 107 with 256 (about
 // 1 us a readout of a tile's 12.8).  The epilogue works on the registers, so the
 // last accumulator is free as early as the others: held until the row's stores
-// are done, the gradient of T = 1024, h = 4096 cost 15 % more.
+// are done, the gradient of T = 1024, h = 4096 cost 15 % more.  The 128 sums of a
+// thread leave 32 to 40 bytes of it spilled at 168 registers.
 constexpr int kChunkKb = 16;
 constexpr bool chunked_k(int epi) { return epi == EPI_LOGP_STATS || epi == EPI_LOGP_GRAD; }
 

@@ -77,8 +77,9 @@ __device__ __forceinline__ uint64_t warp_rth_key(uint64_t key, uint64_t second, 
 // the range is read once more in barrier-separated steps, and whenever kLimit
 // candidates have gathered the threshold is raised among them and the rest
 // dropped.
-// 8192 bf16 rows of 50304 take 141 us without alternatives, 185 at k = 1, 237 at
-// k = 64, 314 at k = 128: the instructions behind a row's last load.  Gathering
+// 8192 bf16 rows of 50304 take 139 us without alternatives, 164 at k = 1, 218 at
+// k = 64, 296 at k = 128: what is behind a row's last load, with no load of that
+// block in flight.  Gathering
 // while streaming, against a threshold from the first elements, took twice the
 // instructions.
 struct Candidates {
@@ -166,7 +167,8 @@ constexpr int kUnits = 4;           // 16-byte units per thread and step
 // of 50304 take 233 us, 7.1 TB/s, with four units a thread and step on eight
 // blocks per SM (two units on ten: 241 us, and 82 against 63 us for 2048 rows,
 // whose last wave has few blocks to keep loads in flight).  bf16 logits take as
-// many instructions for half the bytes: 140 us, 5.9 TB/s.
+// many instructions for half the bytes: 139 us, 5.9 TB/s.  The bf16 kernel with
+// alternatives spills 4 bytes a thread at 72 registers.
 template <typename IT, bool kTop>
 __global__ void __launch_bounds__(kThreads, Unit<IT>::kN == 4 ? 8 : 7)
     logprobs_kernel(const LogprobsArgs a, int slices, int group_log) {
