@@ -2,12 +2,11 @@
 for it run out, the call says so and ends a few limits later, with dozens of rows
 a block still to go, and the context stays usable.  The injection only withholds
 a copy: nothing faults, and every wait ends by its own limit."""
-import time
-
 import pytest
 import torch
 
 import linear_layers_b200 as tpl
+from linear_layers_b200 import build as tpbuild
 from tests.gpu_helpers import guarded
 from tests.logprob_helpers import model_logits
 
@@ -15,6 +14,7 @@ LIMIT = 0.05
 
 
 def test_injection_argument_checks():
+    tpbuild.build()
     with pytest.raises(tpl.TPError):
         tpl.tp_debug_stall_next_distill(-1)
     for us in (0, 10_000_001):
@@ -43,14 +43,16 @@ def test_a_copy_that_never_comes_ends_the_call(dtype, T, v, where):
     out, guard = guarded((T, v), torch.bfloat16)
     loss, loss_guard = guarded((T,), torch.float32)
     st = tpl.new_status()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     torch.cuda.synchronize()
     tpl.tp_debug_stall_next_distill(row, wait_limit_us=int(LIMIT * 1e6))
-    t0 = time.perf_counter()
+    begin.record()
     tpl.vp_distill(x, ids, t, 1, dlogits=out, loss=loss, dev_status=st)
+    end.record()
     torch.cuda.synchronize()
-    took = time.perf_counter() - t0
+    took = begin.elapsed_time(end) * 1e-3
     assert int(st.item()) == tpl.DEVERR_TIMEOUT
-    assert LIMIT <= took < 8 * LIMIT, took     # one block's waits, its peers', the copies'
+    assert LIMIT <= took < 8 * LIMIT, took     # one block's wait, its peers', the copies'
     guard.check("dlogits")
     loss_guard.check("loss")
     assert torch.equal(loss[:row], want["loss"][:row])
